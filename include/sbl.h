@@ -178,6 +178,44 @@ sbl_status sbl_mask_grad(float* dW, const uint8_t* mask_bits, int d_out, int d_i
 sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* workspace,
                            size_t workspace_bytes, void* stream);
 
+/* The global gradient norm over many tensors, and clipping by it (the pages'
+ * grad clip 1.0; same citation as sbl_grad_sqnorm).
+ *   S    = sum over every tensor of g_i^2 (squares exact in fp64, fp64 sums,
+ *          the same bits for the same tensors on one device),
+ *   norm = fl32(sqrt(S)),
+ *   clip = fl32(min(1, max_norm / (sqrt(S) + 1e-6))), computed in fp64,
+ *   out_i = fl32(g_i * clip), rounded once more for a bf16 tensor.
+ * A NaN among the gradients makes norm, clip and every out NaN; an infinity
+ * makes norm infinite and clip 0.
+ * sbl_grad_norm_group writes S and norm; sbl_grad_clip_group writes S, norm,
+ * clip and every out.  S is what sbl_adamw_step takes as grad_sqnorm, so
+ * gradients that go to sbl_adamw_step alone need no clipped copy.
+ *   tensors    HOST array of `count` descriptors (read before the call
+ *              returns; the pointers inside are device pointers, 16-byte
+ *              aligned).  n >= 0 elements, any n; a tensor of n = 0 is
+ *              skipped.  out may be g itself (in place; with clip = 1 nothing
+ *              is then written); it may not overlap any gradient otherwise.
+ *              sbl_grad_norm_group ignores out.
+ *   max_norm   > 0.
+ *   sumsq      1 double out (device, 8-byte aligned).
+ *   norm, clip optional (NULL): 1 float out each (device).
+ *   workspace  device scratch of sbl_grad_group_workspace_bytes(count) bytes,
+ *              256-byte aligned, contents ignored; calls (and replays of
+ *              captured calls) that share one must be ordered. */
+typedef struct {
+  const void* g; /* n gradients, fp32 or bf16 */
+  void* out;     /* n clipped gradients, same type */
+  uint64_t n;
+  int32_t bf16;  /* 1: bf16, 0: fp32 */
+  int32_t reserved; /* 0 */
+} sbl_grad_tensor;
+size_t sbl_grad_group_workspace_bytes(int count);
+sbl_status sbl_grad_norm_group(const sbl_grad_tensor* tensors, int count, double* sumsq, float* norm,
+                               void* workspace, size_t workspace_bytes, void* stream);
+sbl_status sbl_grad_clip_group(const sbl_grad_tensor* tensors, int count, double max_norm,
+                               double* sumsq, float* norm, float* clip, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* sbl_adamw_step: one AdamW update of W, then the weight step of the new W
  * (exactly what sbl_mask_quant would give for it), in two launches; the
  * update shares its read of W with the exact gamma pass.
@@ -266,6 +304,73 @@ sbl_status sbl_act_quant(const void* X, int T, int d_in, int8_t* Xq, float* amax
  *   Xq   [T, d_in] int8 out;  amax [T] float out. */
 sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T, int d_in,
                                  void* Xn, int8_t* Xq, float* amax, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The seam between two products of a block, in one call: the norm of the
+ * branch output, its gate, the scaled residual sum, the norm before the next
+ * product and the activation quantiser.  [summary] Algorithm 1 step (3) for
+ * the norm and the quantiser; the pages do not name the residual, the gate or
+ * a norm after the product, so each of them can be left out.
+ *   r1 = rms(y),  u_j = fl32(fl32(y_j * r1) * g_post_j)      (u = y, r1 = 1 without g_post)
+ *   h'_j = T_rn(fl32(fl32(res_scale * h_j) + fl32(gate_j * u_j)))   (u_j without gate)
+ *   r2 = rms(h'), xn_j = bf16_rn(fl32(fl32(h'_j * r2) * g_pre_j)),
+ *   Xq, amax = Q_a(xn) as sbl_act_quant,
+ * with rms(x) = fl32(1 / fl32(sqrt(fl32(sum x^2 / d + eps)))), the sum in
+ * fp64: no summation order shows in the result (see sbl_rmsnorm_act_quant).
+ * The second norm reads h' as it is stored.  A row that holds a NaN or an
+ * infinity in xn gets it as amax, and codes 0, so that every product of the
+ * row is NaN.
+ *   flags      SBL_BLOCK_Y_BF16: Y is bf16 (else float, as sbl_forward
+ *              writes it); SBL_BLOCK_H_F32: H, H_out (and their gradients)
+ *              are float (else bf16).
+ *   Y, H       [T, d]: the branch output and the residual stream, in.
+ *   g_post     [d] bf16 or NULL.   g_pre  [d] bf16.
+ *   gate       [ceil(T / gate_period), d] bf16 or NULL: token t takes row
+ *              t / gate_period (1: a row for each token; >= T: one row for
+ *              all).  gate_period >= 1, ignored without a gate.
+ *   d          multiple of 16, at most 16384.  T >= 0.
+ *   H_out      [T, d] out, type of H; may be H itself.
+ *   Xn         optional (NULL): [T, d] bf16 out (the input of the dW product).
+ *   Xq, amax   optional, both or neither: [T, d] int8 and [T] float out.
+ *   rstd       optional (NULL): [2, T] float out, r1 then r2 (for the backward).
+ * No other output may overlap an input or another output.
+ *
+ * sbl_block_norm_backward: gradients of all inputs, the quantiser passed by
+ * (straight-through estimator, [summary] 前置知识 (STE)).  With yh = y * r1,
+ * xh = h' * r2, dxn the sum of the `readers` gradients of xn, t = dxn * g_pre:
+ *   dh' = dH_out + r2 * (t - xh * mean(t * xh)),   dH = res_scale * dh',
+ *   du = gate * dh',  dgate = sum over the row's tokens of dh' * yh * g_post,
+ *   dY = r1 * (du * g_post - yh * mean(du * g_post * yh))    (du without g_post),
+ *   dg_pre = sum_t dxn * xh,  dg_post = sum_t du * yh.
+ * fp32 arithmetic, fixed summation order (the same bits on every run), one
+ * rounding where an output is bf16.
+ *   dXn        HOST array of `readers` (1..3) device pointers, [T, d] float
+ *              each: the dX of the products that read xn (sbl_backward).
+ *   dH_out     optional (NULL: zero): [T, d], type of H: the gradient of h'
+ *              from its other readers.
+ *   H_out, rstd, Y, g_post, gate, gate_period, res_scale, g_pre, flags: as
+ *              in the forward call.
+ *   dY         [T, d] bf16 out (the dY of the branch's product).
+ *   dH         optional (NULL): [T, d] out, type of H; may be dH_out itself.
+ *   dg_post, dg_pre [d], dgate [rows of gate, d]: optional (NULL), float out;
+ *              accumulate = 1 adds into the contents, 0 overwrites.
+ *   workspace  device scratch of sbl_block_norm_backward_workspace_bytes(d)
+ *              bytes, 256-byte aligned, contents ignored; calls (and replays
+ *              of captured calls) that share one must be ordered. */
+#define SBL_BLOCK_Y_BF16 1u
+#define SBL_BLOCK_H_F32 2u
+sbl_status sbl_block_norm(const void* Y, const void* H, const void* g_post, const void* gate,
+                          int gate_period, float res_scale, const void* g_pre, float eps, int T,
+                          int d, unsigned flags, void* H_out, void* Xn, int8_t* Xq, float* amax,
+                          float* rstd, void* stream);
+size_t sbl_block_norm_backward_workspace_bytes(int d);
+sbl_status sbl_block_norm_backward(const float* const* dXn, int readers, const void* dH_out,
+                                   const void* Y, const void* H_out, const void* g_post,
+                                   const void* gate, int gate_period, float res_scale,
+                                   const void* g_pre, const float* rstd, int T, int d,
+                                   unsigned flags, void* dY, void* dH, float* dg_post,
+                                   float* dg_pre, float* dgate, int accumulate, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
  * Forward product on int8 tensor cores (tcgen05, int32 accumulation).

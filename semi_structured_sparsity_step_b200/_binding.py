@@ -30,6 +30,12 @@ class GemvProblem(ctypes.Structure):
                 ("d_in", _c_int), ("d_out", _c_int)]
 
 
+class GradTensor(ctypes.Structure):
+    """sbl_grad_tensor: one gradient of a group (device pointers)."""
+    _fields_ = [("g", _vp), ("out", _vp), ("n", ctypes.c_uint64), ("bf16", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "sbl_status_string": (ctypes.c_char_p, [_c_int]),
@@ -44,6 +50,9 @@ SIGNATURES = {
                                    _vp]),
     "sbl_mask_grad": (_c_int, [_vp, _vp, _c_int, _c_int, _vp]),
     "sbl_grad_sqnorm": (_c_int, [_vp, _c_size, _vp, _vp, _c_size, _vp]),
+    "sbl_grad_group_workspace_bytes": (_c_size, [_c_int]),
+    "sbl_grad_norm_group": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_size, _vp]),
+    "sbl_grad_clip_group": (_c_int, [_vp, _c_int, ctypes.c_double, _vp, _vp, _vp, _vp, _c_size, _vp]),
     "sbl_adamw_step": (_c_int, [_vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, ctypes.c_double,
                                 ctypes.c_double, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                 ctypes.c_longlong, _vp, ctypes.c_double, _vp, _vp, _vp, _vp, _vp, _vp, _c_size,
@@ -52,6 +61,11 @@ SIGNATURES = {
     "sbl_mask_quant_noalloc": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _vp]),
     "sbl_act_quant": (_c_int, [_vp, _c_int, _c_int, _vp, _vp, _vp]),
     "sbl_rmsnorm_act_quant": (_c_int, [_vp, _vp, ctypes.c_float, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "sbl_block_norm": (_c_int, [_vp, _vp, _vp, _vp, _c_int, ctypes.c_float, _vp, ctypes.c_float, _c_int, _c_int,
+                                ctypes.c_uint, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "sbl_block_norm_backward_workspace_bytes": (_c_size, [_c_int]),
+    "sbl_block_norm_backward": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, ctypes.c_float, _vp, _vp, _c_int,
+                                         _c_int, ctypes.c_uint, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]),
     "sbl_forward": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "sbl_forward_packed": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "sbl_forward_group": (_c_int, [_vp, _c_int, _vp]),
@@ -125,6 +139,29 @@ def _call(name, *args):
         raise SblError(name, st)
 
 
+class _Args:
+    """Checks the tensor arguments of one call and gives their device pointers.
+
+    A tensor must be on the current device (where the call is launched),
+    contiguous, of the named type and hold at least as many elements as the
+    call touches; anything else raises SBL_ERR_INVALID_ARG before the library
+    is entered.  None and raw pointers (ints) pass through."""
+
+    __slots__ = ("fn", "dev")
+
+    def __init__(self, fn):
+        import torch
+        self.fn = fn
+        self.dev = torch.cuda.current_device()
+
+    def __call__(self, x, dtype, numel):
+        if x is None or isinstance(x, int):
+            return x
+        if x.dtype != dtype or x.numel() < numel or x.get_device() != self.dev or not x.is_contiguous():
+            raise SblError(self.fn, 1)
+        return x.data_ptr()
+
+
 def sbl_status_string(status: int) -> str:
     return load().sbl_status_string(status).decode()
 
@@ -176,6 +213,39 @@ def sbl_grad_sqnorm(dW, n, sumsq, workspace, workspace_bytes, stream=None) -> No
     _call("sbl_grad_sqnorm", _ptr(dW), int(n), _ptr(sumsq), _ptr(workspace), workspace_bytes, _stream(stream))
 
 
+def sbl_grad_group_workspace_bytes(count: int) -> int:
+    return load().sbl_grad_group_workspace_bytes(count)
+
+
+def _grad_tensors(fn, tensors):
+    """tensors: sequence of (g, out_or_None, n, bf16) -> (checker, descriptor array, count)."""
+    import torch
+    a = _Args(fn)
+    words = []
+    for g, out, n, bf16 in tensors:
+        dt = torch.bfloat16 if bf16 else torch.float32
+        # bf16 and the reserved word share the descriptor's last 8 bytes (little-endian)
+        words += (a(g, dt, n) or 0, a(out, dt, n) or 0, n, 1 if bf16 else 0)
+    return a, (ctypes.c_uint64 * max(1, len(words)))(*words), len(words) // 4
+
+
+def sbl_grad_norm_group(tensors, sumsq, norm, workspace, workspace_bytes, stream=None) -> None:
+    """tensors: sequence of (g, None, n, bf16)."""
+    import torch
+    a, arr, count = _grad_tensors("sbl_grad_norm_group", tensors)
+    _call("sbl_grad_norm_group", ctypes.addressof(arr), count, a(sumsq, torch.float64, 1), a(norm, torch.float32, 1),
+          a(workspace, torch.uint8, workspace_bytes), workspace_bytes, _stream(stream))
+
+
+def sbl_grad_clip_group(tensors, max_norm, sumsq, norm, clip, workspace, workspace_bytes, stream=None) -> None:
+    """tensors: sequence of (g, out, n, bf16); out may be g."""
+    import torch
+    a, arr, count = _grad_tensors("sbl_grad_clip_group", tensors)
+    _call("sbl_grad_clip_group", ctypes.addressof(arr), count, max_norm, a(sumsq, torch.float64, 1),
+          a(norm, torch.float32, 1), a(clip, torch.float32, 1), a(workspace, torch.uint8, workspace_bytes),
+          workspace_bytes, _stream(stream))
+
+
 def sbl_adamw_step(W, W32, dW, m, v, d_out, d_in, N, M, lr, beta1, beta2, eps, weight_decay, step, grad_sqnorm,
                    max_norm, W_eff, W_eff_bf16, mask_bits, gamma, flips, workspace, workspace_bytes,
                    stream=None) -> None:
@@ -205,6 +275,47 @@ def sbl_act_quant(X, T, d_in, Xq, amax, stream=None) -> None:
 def sbl_rmsnorm_act_quant(X, g, eps, T, d_in, Xn, Xq, amax, stream=None) -> None:
     _call("sbl_rmsnorm_act_quant", _ptr(X), _ptr(g), float(eps), T, d_in, _ptr(Xn), _ptr(Xq), _ptr(amax),
           _stream(stream))
+
+
+SBL_BLOCK_Y_BF16 = 1
+SBL_BLOCK_H_F32 = 2
+
+
+def _gate_count(gate, gate_period, T):
+    """Rows of the gate that a call on T tokens reads (0 where the period is refused anyway)."""
+    return 0 if gate is None or gate_period < 1 else -(-T // gate_period)
+
+
+def sbl_block_norm(Y, H, g_post, gate, gate_period, res_scale, g_pre, eps, T, d, flags, H_out, Xn, Xq, amax, rstd,
+                   stream=None) -> None:
+    import torch
+    a = _Args("sbl_block_norm")
+    f32, bf16 = torch.float32, torch.bfloat16
+    yt, ht, n = bf16 if flags & SBL_BLOCK_Y_BF16 else f32, f32 if flags & SBL_BLOCK_H_F32 else bf16, T * d
+    _call("sbl_block_norm", a(Y, yt, n), a(H, ht, n), a(g_post, bf16, d),
+          a(gate, bf16, _gate_count(gate, gate_period, T) * d), gate_period, res_scale, a(g_pre, bf16, d), eps, T, d,
+          flags, a(H_out, ht, n), a(Xn, bf16, n), a(Xq, torch.int8, n), a(amax, f32, T), a(rstd, f32, 2 * T),
+          _stream(stream))
+
+
+def sbl_block_norm_backward_workspace_bytes(d) -> int:
+    return load().sbl_block_norm_backward_workspace_bytes(d)
+
+
+def sbl_block_norm_backward(dXn, dH_out, Y, H_out, g_post, gate, gate_period, res_scale, g_pre, rstd, T, d, flags, dY,
+                            dH, dg_post, dg_pre, dgate, accumulate, workspace, workspace_bytes, stream=None) -> None:
+    """dXn: sequence of 1 to 3 gradients of xn (one per product that reads it)."""
+    import torch
+    a = _Args("sbl_block_norm_backward")
+    f32, bf16 = torch.float32, torch.bfloat16
+    yt, ht, n = bf16 if flags & SBL_BLOCK_Y_BF16 else f32, f32 if flags & SBL_BLOCK_H_F32 else bf16, T * d
+    rows = _gate_count(gate, gate_period, T)
+    readers = (_vp * max(1, len(dXn)))(*[a(x, f32, n) for x in dXn])
+    _call("sbl_block_norm_backward", ctypes.addressof(readers), len(dXn), a(dH_out, ht, n), a(Y, yt, n),
+          a(H_out, ht, n), a(g_post, bf16, d), a(gate, bf16, rows * d), gate_period, res_scale, a(g_pre, bf16, d),
+          a(rstd, f32, 2 * T), T, d, flags, a(dY, bf16, n), a(dH, ht, n), a(dg_post, f32, d), a(dg_pre, f32, d),
+          a(dgate, f32, rows * d), int(accumulate),
+          a(workspace, torch.uint8, workspace_bytes), workspace_bytes, _stream(stream))
 
 
 def sbl_forward(Xq, amax, W_eff, gamma, T, d_in, d_out, Y, acc=None, stream=None) -> None:

@@ -1,0 +1,246 @@
+// block_norm.cu -- the seam between two products of a block, forward, in one pass on sm_100a:
+// the norm of the branch output, its gate, the scaled residual sum, the next norm and the int8
+// quantiser.
+//
+// Sparse-BitNet summary ("Sparse-BitNet：1.58-bit 大模型天然兼容半结构化稀疏"), Algorithm 1
+// step (3): the activation is normalised, then quantised to int8.  With the row y of the branch
+// (what the forward product wrote), the residual row h and the token's gate row:
+//   r1 = rms(y),  u_j = fl32(fl32(y_j r1) g_post_j)             (u = y without g_post)
+//   h'_j = T_rn(fl32(fl32(s h_j) + fl32(gate_j u_j)))           (u_j without a gate)
+//   r2 = rms(h'),  xn_j = bf16_rn(fl32(fl32(h'_j r2) g_pre_j)),  then Q_a of the bf16 row xn,
+// where rms(x) = fl32(1 / fl32(sqrt(fl32(sum x^2 / d + eps)))) with the sum in fp64, so no summation
+// order shows in the int8 codes (norm_quant.cu has the argument).
+//
+// HBM bound: one read of y and h, one write of h', xn and the codes.  A row lives in registers
+// (VPT vectors of 4 columns per thread, TPR threads per row) between its three reductions (sum of
+// y^2, sum of h'^2, max |xn|); gains and gate rows come from L1/L2.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "block_norm.cuh"
+#include "sbl_device.cuh"
+#include "sbl_internal.h"
+
+namespace sbl {
+namespace {
+
+constexpr float kBnMagic = 12582912.0f;  // 1.5 * 2^23: one FADD rounds |t| < 2^22 to an integer
+
+struct BlockNormArgs {
+  const void* Y;
+  const void* H;
+  const uint2* g_post;  // 4 bf16 per vector; NULL: no norm of the branch
+  const uint2* gate;    // NULL: no gate
+  const uint2* g_pre;
+  void* H_out;
+  uint2* Xn;      // may be NULL
+  uint32_t* Xq;   // 4 codes per vector; may be NULL (then amax is too)
+  float* amax;
+  float* rstd;    // [2, T]; may be NULL
+  float res_scale, eps;
+  int period, T, nv;  // nv = d / 4
+};
+
+template <int TPR, int THREADS, typename V>
+__device__ __forceinline__ V bn_reduce(V x, V* scratch, int rib, bool is_max) {
+  constexpr int WPR = TPR / 32;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const V y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    x = is_max ? (x > y ? x : y) : x + y;
+  }
+  if constexpr (WPR > 1) {
+    // each reduction of a row has its own scratch, and the barriers of the row's other
+    // reductions keep a fast warp from overwriting it before every warp has read it
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+    __syncthreads();
+    x = scratch[rib * WPR];
+#pragma unroll
+    for (int w = 1; w < WPR; ++w) {
+      const V y = scratch[rib * WPR + w];
+      x = is_max ? (x > y ? x : y) : x + y;
+    }
+  }
+  return x;
+}
+
+__device__ __forceinline__ float bn_rstd(double ss, double d, double eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(static_cast<float>(ss / d + eps)));
+}
+
+template <int TPR, int VPT, bool YB, bool HF>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const BlockNormArgs a) {
+  constexpr int THREADS = TPR < 256 ? 256 : TPR;
+  constexpr int RPB = THREADS / TPR;
+  __shared__ double s_y[THREADS / 32], s_h[THREADS / 32];
+  __shared__ uint32_t s_max[THREADS / 32];
+  const int rib = threadIdx.x / TPR;
+  const int tr = threadIdx.x % TPR;
+  const double d = static_cast<double>(a.nv) * 4.0;
+  const double eps = static_cast<double>(a.eps);
+  pdl::wait();
+
+  for (long long base = static_cast<long long>(blockIdx.x) * RPB; base < a.T;
+       base += static_cast<long long>(gridDim.x) * RPB) {
+    const long long row = base + rib;
+    const bool active = row < a.T;
+    const int rc = static_cast<int>(active ? row : static_cast<long long>(a.T) - 1);
+    const long long at = static_cast<long long>(rc) * a.nv;
+    float y[VPT][4], h[VPT][4];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int i = tr + k * TPR;
+      if (i < a.nv) {
+        load4<YB>(a.Y, at + i, y[k]);
+        load4<!HF>(a.H, at + i, h[k]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[k][j] = h[k][j] = 0.0f;
+      }
+    }
+    float r1 = 1.0f;
+    if (a.g_post != nullptr) {
+      double ss = 0.0;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double v = static_cast<double>(y[k][j]);
+          ss = fma(v, v, ss);
+        }
+      ss = bn_reduce<TPR, THREADS, double>(ss, s_y, rib, false);
+      r1 = bn_rstd(ss, d, eps);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int i = tr + k * TPR;
+        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (i < a.nv) unpack4(__ldg(a.g_post + i), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(__fmul_rn(y[k][j], r1), g[j]);
+      }
+    }
+    if (a.gate != nullptr) {
+      const uint2* gr = a.gate + static_cast<long long>(rc / a.period) * a.nv;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int i = tr + k * TPR;
+        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (i < a.nv) unpack4(__ldg(gr + i), g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(g[j], y[k][j]);
+      }
+    }
+    double ss = 0.0;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int i = tr + k * TPR;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[k][j] = __fadd_rn(__fmul_rn(a.res_scale, h[k][j]), y[k][j]);
+        if constexpr (!HF) h[k][j] = __bfloat162float(__float2bfloat16_rn(h[k][j]));
+      }
+      if (i < a.nv) {
+        if (active) store4<!HF>(a.H_out, at + i, h[k]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const double v = static_cast<double>(h[k][j]);
+          ss = fma(v, v, ss);
+        }
+      }
+    }
+    ss = bn_reduce<TPR, THREADS, double>(ss, s_h, rib, false);
+    const float r2 = bn_rstd(ss, d, eps);
+    uint32_t mx = 0u;
+    uint2 xn[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int i = tr + k * TPR;
+      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (i < a.nv) unpack4(__ldg(a.g_pre + i), g);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[k][j] = __fmul_rn(__fmul_rn(h[k][j], r2), g[j]);
+      xn[k] = pack4(h[k]);
+      if (i < a.nv) {
+        mx = __vmaxu2(mx, __vmaxu2(xn[k].x & 0x7FFF7FFFu, xn[k].y & 0x7FFF7FFFu));
+        if (active && a.Xn != nullptr) a.Xn[at + i] = xn[k];
+      }
+    }
+    mx = max(mx & 0xFFFFu, mx >> 16);
+    mx = bn_reduce<TPR, THREADS, uint32_t>(mx, s_max, rib, true);
+    // magnitudes order like their bits with infinity and NaN on top, so amax is one of them
+    // where the row holds one; its codes are then 0 and every product of the row is NaN
+    float am = __uint_as_float(mx << 16);
+    if (am < 1e-5f) am = 1e-5f;
+    if (active && tr == 0) {
+      if (a.amax != nullptr) a.amax[row] = am;
+      if (a.rstd != nullptr) {
+        a.rstd[row] = r1;
+        a.rstd[a.T + row] = r2;
+      }
+    }
+    if (active && a.Xq != nullptr) {
+      const bool finite = mx < 0x7F80u;
+      const float sc = __fdiv_rn(127.0f, am);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int i = tr + k * TPR;
+        if (i >= a.nv) continue;
+        float x[4];
+        unpack4(xn[k], x);
+        uint32_t q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], sc), kBnMagic));
+        const uint32_t w = __byte_perm(__byte_perm(q[0], q[1], 0x0040u), __byte_perm(q[2], q[3], 0x0040u), 0x5410u);
+        a.Xq[at + i] = finite ? w : 0u;
+      }
+    }
+  }
+}
+
+template <int TPR, int VPT, bool YB, bool HF>
+cudaError_t run(const BlockNormArgs& a, int blocks_per_sm, cudaStream_t stream, int num_sms) {
+  constexpr int THREADS = TPR < 256 ? 256 : TPR;
+  constexpr int RPB = THREADS / TPR;
+  long long blocks = (static_cast<long long>(a.T) + RPB - 1) / RPB;
+  const long long cap = static_cast<long long>(num_sms) * blocks_per_sm;
+  if (blocks > cap) blocks = cap;
+  return pdl::launch(block_norm_kernel<TPR, VPT, YB, HF>, static_cast<int>(blocks), THREADS, 0, 1, stream, a);
+}
+
+template <bool YB, bool HF>
+cudaError_t dispatch(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
+  if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 8, stream, num_sms);
+  if (a.nv <= 64 * 2) return run<64, 2, YB, HF>(a, 8, stream, num_sms);
+  if (a.nv <= 128 * 2) return run<128, 2, YB, HF>(a, 8, stream, num_sms);
+  if (a.nv <= 256 * 2) return run<256, 2, YB, HF>(a, 8, stream, num_sms);
+  if (a.nv <= 512 * 2) return run<512, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 512 * 4) return run<512, 4, YB, HF>(a, 4, stream, num_sms);
+  return run<512, 8, YB, HF>(a, 4, stream, num_sms);
+}
+
+}  // namespace
+
+cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms) {
+  if (p.T == 0) return cudaSuccess;
+  BlockNormArgs a{};
+  a.Y = p.Y;
+  a.H = p.H;
+  a.g_post = static_cast<const uint2*>(p.g_post);
+  a.gate = static_cast<const uint2*>(p.gate);
+  a.g_pre = static_cast<const uint2*>(p.g_pre);
+  a.H_out = p.H_out;
+  a.Xn = static_cast<uint2*>(p.Xn);
+  a.Xq = reinterpret_cast<uint32_t*>(p.Xq);
+  a.amax = p.amax;
+  a.rstd = p.rstd;
+  a.res_scale = p.res_scale;
+  a.eps = p.eps;
+  a.period = p.gate_period;
+  a.T = p.T;
+  a.nv = p.d / 4;
+  if (p.y_bf16) return p.h_f32 ? dispatch<true, true>(a, stream, num_sms) : dispatch<true, false>(a, stream, num_sms);
+  return p.h_f32 ? dispatch<false, true>(a, stream, num_sms) : dispatch<false, false>(a, stream, num_sms);
+}
+
+}  // namespace sbl

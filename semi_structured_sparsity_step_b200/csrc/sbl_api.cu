@@ -3,6 +3,7 @@
 // dispatch to the kernels' launchers.  Nothing here allocates device memory.
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <vector>
@@ -204,6 +205,50 @@ sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* works
   return from_cuda(launch_grad_sqnorm(dW, n, sumsq, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t sbl_grad_group_workspace_bytes(int count) { return count < 0 ? 0 : grad_group_workspace_bytes(count); }
+
+static sbl_status grad_group(const sbl_grad_tensor* tensors, int count, bool clip_them, double max_norm,
+                             double* sumsq, float* norm, float* clip, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (count < 0 || (count > 0 && tensors == nullptr) || sumsq == nullptr || workspace == nullptr)
+    return SBL_ERR_INVALID_ARG;
+  if (clip_them && !(max_norm > 0.0)) return SBL_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const sbl_grad_tensor& t = tensors[i];
+    if ((t.bf16 != 0 && t.bf16 != 1) || t.reserved != 0) return SBL_ERR_INVALID_ARG;
+    if (t.n == 0) continue;
+    if (t.n > (1ull << 40)) return SBL_ERR_SHAPE;
+    if (t.g == nullptr || (clip_them && t.out == nullptr)) return SBL_ERR_INVALID_ARG;
+    if (!aligned16(t.g) || (clip_them && !aligned16(t.out))) return SBL_ERR_ALIGN;
+  }
+  if ((reinterpret_cast<uintptr_t>(sumsq) & 7u) != 0 || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0 ||
+      (reinterpret_cast<uintptr_t>(clip) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return SBL_ERR_ALIGN;
+  if (workspace_bytes < grad_group_workspace_bytes(count)) return SBL_ERR_WORKSPACE;
+  DeviceInfo* d = nullptr;
+  const sbl_status st = current_device(&d);
+  if (st != SBL_OK) return st;
+  try {
+    std::vector<GradTensorDev> dev(static_cast<size_t>(count));
+    for (int i = 0; i < count; ++i)
+      dev[i] = GradTensorDev{tensors[i].g, tensors[i].out, tensors[i].n, tensors[i].bf16 != 0};
+    return from_cuda(launch_grad_group(dev.data(), count, clip_them, max_norm, sumsq, norm, clip, workspace,
+                                       static_cast<cudaStream_t>(stream), d->num_sms));
+  } catch (...) {  // no host memory for the descriptors: no exception crosses the ABI
+    return SBL_ERR_CUDA;
+  }
+}
+
+sbl_status sbl_grad_norm_group(const sbl_grad_tensor* tensors, int count, double* sumsq, float* norm,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  return grad_group(tensors, count, false, 0.0, sumsq, norm, nullptr, workspace, workspace_bytes, stream);
+}
+
+sbl_status sbl_grad_clip_group(const sbl_grad_tensor* tensors, int count, double max_norm, double* sumsq,
+                               float* norm, float* clip, void* workspace, size_t workspace_bytes, void* stream) {
+  return grad_group(tensors, count, true, max_norm, sumsq, norm, clip, workspace, workspace_bytes, stream);
+}
+
 sbl_status sbl_adamw_step(void* W, float* W32, const float* dW, float* m, float* v, int d_out, int d_in, int N,
                           int M, double lr, double beta1, double beta2, double eps, double weight_decay,
                           long long step, const double* grad_sqnorm, double max_norm, int8_t* W_eff,
@@ -258,6 +303,104 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
   if (st != SBL_OK) return st;
   return from_cuda(launch_norm_act_quant(X, g, eps, T, d_in, Xn, Xq, amax, static_cast<cudaStream_t>(stream),
                                          d->num_sms));
+}
+
+static sbl_status check_block_norm(const void* g_pre, const void* gate, int gate_period, float res_scale, int T,
+                                   int d, unsigned flags) {
+  if ((flags & ~(SBL_BLOCK_Y_BF16 | SBL_BLOCK_H_F32)) != 0u) return SBL_ERR_INVALID_ARG;
+  if (T < 0 || d <= 0 || d % 16 != 0 || d > kBlockNormMaxWidth) return SBL_ERR_SHAPE;
+  if (!std::isfinite(res_scale) || (gate != nullptr && gate_period < 1)) return SBL_ERR_INVALID_ARG;
+  if (T > 0 && g_pre == nullptr) return SBL_ERR_INVALID_ARG;
+  return SBL_OK;
+}
+
+sbl_status sbl_block_norm(const void* Y, const void* H, const void* g_post, const void* gate, int gate_period,
+                          float res_scale, const void* g_pre, float eps, int T, int d, unsigned flags, void* H_out,
+                          void* Xn, int8_t* Xq, float* amax, float* rstd, void* stream) {
+  sbl_status st = check_block_norm(g_pre, gate, gate_period, res_scale, T, d, flags);
+  if (st != SBL_OK) return st;
+  if (!(eps > 0.0f)) return SBL_ERR_INVALID_ARG;
+  if (T == 0) return SBL_OK;
+  if (Y == nullptr || H == nullptr || H_out == nullptr || (Xq == nullptr) != (amax == nullptr))
+    return SBL_ERR_INVALID_ARG;
+  if (!aligned16(Y) || !aligned16(H) || !aligned16(g_post) || !aligned16(gate) || !aligned16(g_pre) ||
+      !aligned16(H_out) || !aligned16(Xn) || !aligned16(Xq) || !aligned16(amax) || !aligned16(rstd))
+    return SBL_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != SBL_OK) return st;
+  BlockNormDev p{};
+  p.Y = Y;
+  p.H = H;
+  p.g_post = g_post;
+  p.gate = gate;
+  p.g_pre = g_pre;
+  p.H_out = H_out;
+  p.Xn = Xn;
+  p.Xq = Xq;
+  p.amax = amax;
+  p.rstd = rstd;
+  p.res_scale = res_scale;
+  p.eps = eps;
+  p.gate_period = gate != nullptr ? gate_period : 1;
+  p.T = T;
+  p.d = d;
+  p.y_bf16 = (flags & SBL_BLOCK_Y_BF16) != 0u;
+  p.h_f32 = (flags & SBL_BLOCK_H_F32) != 0u;
+  return from_cuda(launch_block_norm(p, static_cast<cudaStream_t>(stream), dev->num_sms));
+}
+
+size_t sbl_block_norm_backward_workspace_bytes(int d) {
+  return d <= 0 || d % 16 != 0 || d > kBlockNormMaxWidth ? 0 : block_norm_bwd_workspace_bytes(d);
+}
+
+sbl_status sbl_block_norm_backward(const float* const* dXn, int readers, const void* dH_out, const void* Y,
+                                   const void* H_out, const void* g_post, const void* gate, int gate_period,
+                                   float res_scale, const void* g_pre, const float* rstd, int T, int d,
+                                   unsigned flags, void* dY, void* dH, float* dg_post, float* dg_pre, float* dgate,
+                                   int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  sbl_status st = check_block_norm(g_pre, gate, gate_period, res_scale, T, d, flags);
+  if (st != SBL_OK) return st;
+  if (readers < 1 || readers > 3 || dXn == nullptr || (accumulate != 0 && accumulate != 1))
+    return SBL_ERR_INVALID_ARG;
+  if ((dg_post != nullptr && g_post == nullptr) || (dgate != nullptr && gate == nullptr)) return SBL_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (Y == nullptr || H_out == nullptr || rstd == nullptr || dY == nullptr) return SBL_ERR_INVALID_ARG;
+    for (int i = 0; i < readers; ++i)
+      if (dXn[i] == nullptr) return SBL_ERR_INVALID_ARG;
+  }
+  if (workspace == nullptr) return SBL_ERR_INVALID_ARG;
+  bool al = aligned16(dH_out) && aligned16(Y) && aligned16(H_out) && aligned16(g_post) && aligned16(gate) &&
+            aligned16(g_pre) && aligned16(rstd) && aligned16(dY) && aligned16(dH) && aligned16(dg_post) &&
+            aligned16(dg_pre) && aligned16(dgate) && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0;
+  for (int i = 0; i < readers; ++i) al = al && aligned16(dXn[i]);
+  if (!al) return SBL_ERR_ALIGN;
+  if (workspace_bytes < block_norm_bwd_workspace_bytes(d)) return SBL_ERR_WORKSPACE;
+  DeviceInfo* dev = nullptr;
+  if ((st = current_device(&dev)) != SBL_OK) return st;
+  BlockNormBwdDev p{};
+  for (int i = 0; i < readers; ++i) p.dXn[i] = dXn[i];
+  p.readers = readers;
+  p.dH_out = dH_out;
+  p.Y = Y;
+  p.H_out = H_out;
+  p.g_post = g_post;
+  p.gate = gate;
+  p.g_pre = g_pre;
+  p.rstd = rstd;
+  p.dY = dY;
+  p.dH = dH;
+  p.dg_post = dg_post;
+  p.dg_pre = dg_pre;
+  p.dgate = dgate;
+  p.res_scale = res_scale;
+  p.gate_period = gate != nullptr ? gate_period : 1;
+  p.T = T;
+  p.d = d;
+  p.accumulate = accumulate;
+  p.y_bf16 = (flags & SBL_BLOCK_Y_BF16) != 0u;
+  p.h_f32 = (flags & SBL_BLOCK_H_F32) != 0u;
+  p.workspace = workspace;
+  return from_cuda(launch_block_norm_bwd(p, static_cast<cudaStream_t>(stream), dev->num_sms));
 }
 
 sbl_status sbl_forward(const int8_t* Xq, const float* amax, const int8_t* W_eff, const float* gamma, int T,

@@ -44,11 +44,49 @@ cudaError_t launch_adamw_step(void* W, float* W32, const float* dW, float* m, fl
 // *sumsq += sum of g^2 (fp64, deterministic for a given n).
 cudaError_t launch_grad_sqnorm(const float* g, size_t n, double* sumsq, void* workspace, cudaStream_t stream);
 
+// ---- the global gradient norm over many tensors, and clipping (grad_group.cu)
+struct GradTensorDev {
+  const void* g;
+  void* out;
+  unsigned long long n;
+  bool bf16;
+};
+size_t grad_group_workspace_bytes(int count);
+cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them, double max_norm, double* sumsq,
+                              float* norm, float* clip, void* workspace, cudaStream_t stream, int num_sms);
+
 // ---- activation quantiser (act_quant.cu)
 cudaError_t launch_norm_act_quant(const void* X, const void* g, float eps, int T, int d_in, void* Xn, int8_t* Xq,
                                   float* amax, cudaStream_t stream, int num_sms);
 cudaError_t launch_act_quant(const void* X, int T, int d_in, int8_t* Xq, float* amax, cudaStream_t stream,
                              int num_sms);
+
+// ---- the block norm and its backward (block_norm.cu, block_norm_bwd.cu)
+struct BlockNormDev {
+  const void *Y, *H, *g_post, *gate, *g_pre;
+  void *H_out, *Xn;
+  int8_t* Xq;
+  float *amax, *rstd;
+  float res_scale, eps;
+  int gate_period, T, d;
+  bool y_bf16, h_f32;
+};
+cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms);
+struct BlockNormBwdDev {
+  const float* dXn[3];
+  int readers;
+  const void *dH_out, *Y, *H_out, *g_post, *gate, *g_pre;
+  const float* rstd;
+  void *dY, *dH;
+  float *dg_post, *dg_pre, *dgate;
+  float res_scale;
+  int gate_period, T, d, accumulate;
+  bool y_bf16, h_f32;
+  void* workspace;
+};
+constexpr int kBlockNormMaxWidth = 16384;
+size_t block_norm_bwd_workspace_bytes(int d);
+cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream, int num_sms);
 
 // ---- tensor-core GEMMs (gemm_tc.cu)
 // 2-D tensor map of a row-major [rows, inner] uint32 matrix (row stride in

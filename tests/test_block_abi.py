@@ -1,0 +1,113 @@
+"""Refusals of the block norm and the group clip: on the host, before a device is needed."""
+import ctypes
+import math
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def cl():
+    from semi_structured_sparsity_step_b200 import build
+    build.build()
+    from semi_structured_sparsity_step_b200 import _binding
+    return _binding.load()
+
+
+AL = 1 << 12  # a fake aligned address: never dereferenced on these paths
+
+
+def _norm(cl, **kw):
+    a = dict(Y=AL, H=AL, g_post=AL, gate=None, period=0, s=1.0, g_pre=AL, eps=1e-6, T=4, d=32, flags=0, H_out=AL,
+             Xn=AL, Xq=AL, amax=AL, rstd=AL)
+    a.update(kw)
+    return cl.sbl_block_norm(*a.values(), None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (1, dict(flags=4)), (1, dict(eps=0.0)), (1, dict(eps=math.nan)), (1, dict(s=math.inf)), (1, dict(s=math.nan)),
+    (1, dict(gate=AL, period=0)), (1, dict(gate=AL, period=-1)), (1, dict(Y=None)), (1, dict(H=None)),
+    (1, dict(H_out=None)), (1, dict(g_pre=None)), (1, dict(Xq=None)), (1, dict(amax=None)),
+    (2, dict(T=-1)), (2, dict(d=24)), (2, dict(d=0)), (2, dict(d=-16)), (2, dict(d=16400)),
+    (3, dict(Y=AL + 8)), (3, dict(H=AL + 4)), (3, dict(gate=AL + 2, period=1)), (3, dict(rstd=AL + 4)),
+    (3, dict(Xn=AL + 8)), (0, dict(T=0)),
+])
+def test_block_norm_refuses(cl, status, kw):
+    assert _norm(cl, **kw) == status
+
+
+def _bwd(cl, readers=1, n_ptr=None, **kw):
+    ptrs = (ctypes.c_void_p * 4)(*([AL] * 4 if n_ptr is None else n_ptr))
+    a = dict(dXn=ctypes.addressof(ptrs), readers=readers, dH_out=AL, Y=AL, H_out=AL, g_post=AL, gate=None, period=0,
+             s=1.0, g_pre=AL, rstd=AL, T=4, d=32, flags=0, dY=AL, dH=AL, dg_post=AL, dg_pre=AL, dgate=None, acc=0,
+             ws=AL, ws_bytes=1 << 30)
+    a.update(kw)
+    return cl.sbl_block_norm_backward(*a.values(), None)
+
+
+@pytest.mark.parametrize("status,kw", [
+    (1, dict(readers=0)), (1, dict(readers=4)), (1, dict(dXn=None)), (1, dict(readers=2, n_ptr=[AL, None, AL, AL])),
+    (1, dict(flags=8)), (1, dict(acc=2)), (1, dict(g_post=None)), (1, dict(dgate=AL)), (1, dict(s=math.inf)),
+    (1, dict(Y=None)), (1, dict(H_out=None)), (1, dict(rstd=None)), (1, dict(dY=None)), (1, dict(ws=None)),
+    (1, dict(gate=AL, period=0)), (2, dict(T=-1)), (2, dict(d=8)), (2, dict(d=16400)),
+    (3, dict(Y=AL + 8)), (3, dict(n_ptr=[AL + 4, AL, AL, AL])), (3, dict(ws=AL + 16)), (3, dict(dg_pre=AL + 4)),
+    (5, dict(ws_bytes=16)),
+])
+def test_block_norm_backward_refuses(cl, status, kw):
+    assert _bwd(cl, **kw) == status
+
+
+def test_block_norm_backward_workspace(cl):
+    assert cl.sbl_block_norm_backward_workspace_bytes(0) == 0
+    assert cl.sbl_block_norm_backward_workspace_bytes(20) == 0
+    assert cl.sbl_block_norm_backward_workspace_bytes(16400) == 0
+    for d in (16, 256, 272, 896, 2048, 2064, 8192, 16384):
+        assert 0 < cl.sbl_block_norm_backward_workspace_bytes(d) <= 64 << 20
+
+
+def _clip(cl, tensors, count=None, max_norm=1.0, sumsq=AL, norm=AL, clip=AL, ws=AL, ws_bytes=1 << 30):
+    from semi_structured_sparsity_step_b200 import _binding as B
+    arr = (B.GradTensor * max(1, len(tensors)))(*[B.GradTensor(*t) for t in tensors])
+    return cl.sbl_grad_clip_group(ctypes.addressof(arr), len(tensors) if count is None else count, max_norm, sumsq,
+                                  norm, clip, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("status,tensors,kw", [
+    (1, [(AL, AL, 4, 2, 0)], {}), (1, [(AL, AL, 4, 0, 7)], {}), (1, [(None, AL, 4, 0, 0)], {}),
+    (1, [(AL, None, 4, 0, 0)], {}), (1, [], dict(count=-1)), (1, [(AL, AL, 4, 0, 0)], dict(max_norm=0.0)),
+    (1, [(AL, AL, 4, 0, 0)], dict(max_norm=math.nan)), (1, [(AL, AL, 4, 0, 0)], dict(sumsq=None)),
+    (1, [(AL, AL, 4, 0, 0)], dict(ws=None)), (2, [(AL, AL, 1 << 41, 0, 0)], {}),
+    (3, [(AL + 8, AL, 4, 0, 0)], {}), (3, [(AL, AL + 4, 4, 1, 0)], {}), (3, [(AL, AL, 4, 0, 0)], dict(sumsq=AL + 4)),
+    (3, [(AL, AL, 4, 0, 0)], dict(ws=AL + 16)), (3, [(AL, AL, 4, 0, 0)], dict(clip=AL + 2)),
+    (5, [(AL, AL, 4, 0, 0)], dict(ws_bytes=64)), (5, [(AL, AL, 4, 0, 0)] * 200, dict(ws_bytes=1 << 14)),
+])
+def test_grad_clip_group_refuses(cl, status, tensors, kw):
+    assert _clip(cl, tensors, **kw) == status
+
+
+def test_grad_norm_group_refuses_and_ignores_out(cl):
+    from semi_structured_sparsity_step_b200 import _binding as B
+    t = (B.GradTensor * 1)(B.GradTensor(AL + 4, None, 4, 0, 0))
+    assert cl.sbl_grad_norm_group(ctypes.addressof(t), 1, AL, AL, AL, 1 << 30, None) == 3
+    t[0].g = None
+    assert cl.sbl_grad_norm_group(ctypes.addressof(t), 1, AL, AL, AL, 1 << 30, None) == 1
+    assert cl.sbl_grad_norm_group(None, 1, AL, AL, AL, 1 << 30, None) == 1
+    assert cl.sbl_grad_group_workspace_bytes(-1) == 0
+    assert cl.sbl_grad_group_workspace_bytes(129) > cl.sbl_grad_group_workspace_bytes(128)
+
+
+def test_binding_refuses_tensors_that_the_call_would_misread(monkeypatch):
+    """A host tensor, a wrong type, a strided view and a short buffer never reach the library."""
+    import torch
+    from semi_structured_sparsity_step_b200 import _binding as B
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    a = B._Args("sbl_block_norm")
+    assert a(None, torch.float32, 4) is None and a(AL, torch.float32, 4) == AL
+    with pytest.raises(B.SblError):
+        a(torch.zeros(4), torch.float32, 4)  # on the host
+    a.dev = -1  # what get_device() gives for the host tensors below
+    x = torch.zeros(4, 8)
+    assert a(x, torch.float32, 32) == x.data_ptr()
+    for bad in (x.to(torch.bfloat16), x[:, ::2], x[:2], x.t()):
+        with pytest.raises(B.SblError) as e:
+            a(bad, torch.float32, 32)
+        assert e.value.status == 1
