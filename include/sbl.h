@@ -459,6 +459,30 @@ sbl_status sbl_forward_sparse24(const int8_t* Xq, const float* amax, const uint8
                                 int32_t* acc, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The 8-bit product, for projections that are not ternary (an output head,
+ * the first and last layers): int8 activations with a scale for each token,
+ * int8 weights with a scale for each output channel.  [summary] 前置知识 for
+ * the activations (absmax to 8 bits); the pages quantise no weight to 8 bits.
+ *   acc[t, o] = sum_j Xq[t, j] * Wq[o, j]   (exact int32),
+ *   Y[t, o] = T_rn(fl32(fl32(fl32(acc) * fl32(amax_t / 127)) * fl32(wmax_o / 127))).
+ * The weight is quantised once by sbl_act_quant on its rows: Wq, wmax =
+ * Q_a(W) with T = d_out.  Training such a layer with the straight-through
+ * estimator is sbl_backward on the bf16 W with gamma = 1.
+ * One call serves every T: short batches (decode, a short prefill) run a
+ * kernel that streams Wq once over all SMs, full ones the CTA-pair kernel of
+ * sbl_forward; the results do not depend on which (exact sums, the same
+ * scaling).
+ *   Xq [T, d_in] int8, amax [T] float (sbl_act_quant, sbl_block_norm),
+ *   Wq [d_out, d_in] int8, wmax [d_out] float; codes may take any int8 value.
+ *   d_in >= 16, at most 131056 (int32 sums cannot overflow).
+ *   flags      SBL_W8A8_Y_BF16: Y is bf16, else float.
+ *   Y          [T, d_out] out. */
+#define SBL_W8A8_Y_BF16 1u
+sbl_status sbl_forward_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq,
+                            const float* wmax, int T, int d_in, int d_out, unsigned flags, void* Y,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
  * Dual-STE backward on bf16 tensor cores (tcgen05, fp32 accumulation).
  * [summary] 前置知识 / STE and 核心方法 (masked weights receive the full
  * gradient), Algorithm 1 step (7):

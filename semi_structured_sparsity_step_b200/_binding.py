@@ -67,6 +67,7 @@ SIGNATURES = {
     "sbl_block_norm_backward": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, ctypes.c_float, _vp, _vp, _c_int,
                                          _c_int, ctypes.c_uint, _vp, _vp, _vp, _vp, _vp, _c_int, _vp, _c_size, _vp]),
     "sbl_forward": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
+    "sbl_forward_w8a8": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, ctypes.c_uint, _vp, _vp]),
     "sbl_forward_packed": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp]),
     "sbl_forward_group": (_c_int, [_vp, _c_int, _vp]),
     "sbl_compress24_bytes": (_c_size, [_c_int, _c_int]),
@@ -329,6 +330,17 @@ def sbl_forward_group(problems, stream=None) -> None:
     for i, (xq, am, w, g, T, d_in, d_out, y, acc) in enumerate(problems):
         arr[i] = ForwardProblem(_ptr(xq), _ptr(am), _ptr(w), _ptr(g), T, d_in, d_out, _ptr(y), _ptr(acc))
     _call("sbl_forward_group", ctypes.cast(arr, _vp), len(problems), _stream(stream))
+
+
+SBL_W8A8_Y_BF16 = 1
+
+
+def sbl_forward_w8a8(Xq, amax, Wq, wmax, T, d_in, d_out, flags, Y, stream=None) -> None:
+    import torch
+    a = _Args("sbl_forward_w8a8")
+    f32, i8 = torch.float32, torch.int8
+    _call("sbl_forward_w8a8", a(Xq, i8, T * d_in), a(amax, f32, T), a(Wq, i8, d_out * d_in), a(wmax, f32, d_out), T,
+          d_in, d_out, flags, a(Y, torch.bfloat16 if flags & SBL_W8A8_Y_BF16 else f32, T * d_out), _stream(stream))
 
 
 def sbl_forward_packed(Xq, amax, packed, gamma, T, d_in, d_out, N, M, Y, acc=None, stream=None) -> None:

@@ -3,6 +3,8 @@
 //   (a5) forward, int8 x int8 -> int32 (kind::i8):
 //        acc[t,o] = sum_j Xq[t,j] W_eff[o,j];  Y = fp32(acc) * fp32(gamma * fp32(amax_t / 127))
 //        Sparse-BitNet summary, Algorithm 1 step (6).
+//   8-bit product of a full batch (gemm_w8a8.cu has the short ones): the forward with the scale
+//        fl32(amax_t / 127) of each token and fl32(wmax_o / 127) of each weight row.
 //   (a6) dX = gamma * (dY . W_eff), bf16 x bf16 -> fp32 (kind::f16)
 //   (a7) dW = dY^T . X (dense, every position of W), bf16 x bf16 -> fp32
 //        Sparse-BitNet summary, STE (前置知识) and 核心方法, Algorithm 1 step (7).
@@ -25,6 +27,7 @@
 //   * every mbarrier wait is bounded (sbl_device.cuh) and unwinds with a
 //     latched error instead of hanging.
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <atomic>
@@ -42,7 +45,9 @@ namespace {
 constexpr int BM = 128;
 constexpr int kThreads = 192;
 
-enum Epi : int { kEpiFwd = 0, kEpiDx = 1, kEpiDw = 2 };
+// kEpiW8F32 / kEpiW8Bf16: the 8-bit product, scaled per token and per output channel, in either type.
+enum Epi : int { kEpiFwd = 0, kEpiDx = 1, kEpiDw = 2, kEpiW8F32 = 3, kEpiW8Bf16 = 4 };
+constexpr bool epi_w8(int e) { return e == kEpiW8F32 || e == kEpiW8Bf16; }
 
 // Programmatic dependent launch: a product may start while the previous
 // kernel of its stream finishes.  The prologue (barriers, tensor memory,
@@ -60,6 +65,7 @@ struct GemmArgs {
   int32_t* acc_out;
   const float* amax;
   const float* gamma;
+  const float* wmax;  // 8-bit product: largest magnitude of each weight row
   int accumulate;  // dW: add into `out`
   int atomic_out;  // split-K: atomically add into `out`
   int atomic_i32;  // forward split-K: add the int32 partial sums, as exact fp32 integers, into `out`
@@ -114,6 +120,8 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
     if constexpr (EPI == kEpiFwd) {
       v = a.atomic_i32 ? __int2float_rn(static_cast<int>(r[j]))
                        : __fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale);
+    } else if constexpr (epi_w8(EPI)) {
+      v = __fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale);
     } else if constexpr (EPI == kEpiDx) {
       v = __fmul_rn(scale, __uint_as_float(r[j]));
     } else {
@@ -133,6 +141,14 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
   }
   __syncwarp();
   const int cq = (lane & 7) * 4;
+  float4 sw = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // 8-bit product: the scales of this lane's four columns
+  if constexpr (epi_w8(EPI)) {
+    if (col0 + cq < a.N) {
+      const float4 w = __ldg(reinterpret_cast<const float4*>(a.wmax + col0 + cq));
+      sw = make_float4(__fdiv_rn(w.x, 127.0f), __fdiv_rn(w.y, 127.0f), __fdiv_rn(w.z, 127.0f),
+                       __fdiv_rn(w.w, 127.0f));
+    }
+  }
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int rr = it * 4 + (lane >> 3);
@@ -141,6 +157,15 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
     if (grow < a.M && gcol < a.N) {  // N % 8 == 0: a float4 is either all in or all out
       const float* t = tile + rr * 33 + cq;
       float4 v = make_float4(t[0], t[1], t[2], t[3]);
+      if constexpr (epi_w8(EPI))
+        v = make_float4(__fmul_rn(v.x, sw.x), __fmul_rn(v.y, sw.y), __fmul_rn(v.z, sw.z), __fmul_rn(v.w, sw.w));
+      if constexpr (EPI == kEpiW8Bf16) {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(grow) * a.ldo +
+                                  gcol) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        continue;
+      }
       float* dst = a.out + static_cast<long long>(grow) * a.ldo + gcol;
       if constexpr (EPI == kEpiFwd) {
         if (a.atomic_i32) {
@@ -711,6 +736,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
       float scale = 0.0f;
       if constexpr (EPI == kEpiFwd) {
         if (row < A.M) scale = __fmul_rn(*A.gamma, __fdiv_rn(A.amax[row], 127.0f));
+      } else if constexpr (epi_w8(EPI)) {
+        if (row < A.M) scale = __fdiv_rn(A.amax[row], 127.0f);
       } else if constexpr (EPI == kEpiDx) {
         scale = *A.gamma;
       }
@@ -991,6 +1018,27 @@ cudaError_t launch_forward(const int8_t* Xq, const float* amax, const int8_t* W_
                                                              static_cast<double>(d_out) * d_in);
   }
   return run<true, false, false, kBN, kStages, kEpiFwd>(ta, tb, a, 1, num_sms, stream);
+}
+
+cudaError_t launch_forward_w8a8_pair(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T,
+                                     int d_in, int d_out, bool y_bf16, void* Y, cudaStream_t stream, int num_sms,
+                                     uint32_t* err) {
+  CUtensorMap ta, tb;
+  if (!make_tmap(&ta, Xq, false, d_in, T, d_in, 128, BM)) return cudaErrorInvalidValue;
+  if (!make_tmap(&tb, Wq, false, d_in, d_out, d_in, 128, 128)) return cudaErrorInvalidValue;
+  GemmArgs a{};
+  a.M = T;
+  a.N = d_out;
+  a.K = d_in;
+  a.kb_per_split = (d_in + 127) / 128;
+  a.out = static_cast<float*>(Y);
+  a.ldo = d_out;
+  a.amax = amax;
+  a.wmax = wmax;
+  a.err = err;
+  const double ab = static_cast<double>(T) * d_in, bb = static_cast<double>(d_out) * d_in;
+  return y_bf16 ? run_pair<true, false, false, kPairStages, kEpiW8Bf16>(ta, tb, a, 1, num_sms, stream, ab, bb)
+                : run_pair<true, false, false, kPairStages, kEpiW8F32>(ta, tb, a, 1, num_sms, stream, ab, bb);
 }
 
 cudaError_t launch_forward_group(const FwdProblemDev* probs, int count, cudaStream_t stream, int num_sms,

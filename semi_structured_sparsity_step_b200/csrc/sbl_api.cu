@@ -446,6 +446,22 @@ sbl_status sbl_forward_group(const sbl_forward_problem* problems, int count, voi
                                         d->num_sms, d->err));
 }
 
+sbl_status sbl_forward_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T, int d_in,
+                            int d_out, unsigned flags, void* Y, void* stream) {
+  if ((flags & ~SBL_W8A8_Y_BF16) != 0u) return SBL_ERR_INVALID_ARG;
+  sbl_status st = check_dims(d_in, d_out);
+  if (st != SBL_OK) return st;
+  if (T < 0 || d_in == 0 || d_in >= (1 << 17)) return SBL_ERR_SHAPE;
+  if (T == 0 || d_out == 0) return SBL_OK;
+  if (Xq == nullptr || amax == nullptr || Wq == nullptr || wmax == nullptr || Y == nullptr)
+    return SBL_ERR_INVALID_ARG;
+  if (!aligned16(Xq) || !aligned16(amax) || !aligned16(Wq) || !aligned16(wmax) || !aligned16(Y)) return SBL_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  if ((st = current_device(&d)) != SBL_OK) return st;
+  return from_cuda(launch_w8a8(Xq, amax, Wq, wmax, T, d_in, d_out, (flags & SBL_W8A8_Y_BF16) != 0u, Y,
+                               static_cast<cudaStream_t>(stream), d->num_sms, d->err));
+}
+
 sbl_status sbl_forward_packed(const int8_t* Xq, const float* amax, const uint8_t* packed, const float* gamma,
                               int T, int d_in, int d_out, int N, int M, float* Y, int32_t* acc, void* stream) {
   sbl_status st = check_nm(N, M);

@@ -119,6 +119,14 @@ cudaError_t launch_backward(const void* dY, const void* X, const void* W_eff_bf1
                             int d_in, int d_out, float* dX, float* dW, int accumulate_dW, cudaStream_t stream,
                             int num_sms, uint32_t* err);
 
+// The 8-bit product with a scale per token and per output channel (gemm_w8a8.cu), and its full-batch
+// form on CTA pairs (gemm_tc.cu).
+cudaError_t launch_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T, int d_in,
+                        int d_out, bool y_bf16, void* Y, cudaStream_t stream, int num_sms, uint32_t* err);
+cudaError_t launch_forward_w8a8_pair(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T,
+                                     int d_in, int d_out, bool y_bf16, void* Y, cudaStream_t stream, int num_sms,
+                                     uint32_t* err);
+
 // ---- 2:4 compressed weight and the sparse tensor-core forward (gemm_sp24.cu)
 size_t sparse24_values_row_bytes(int d_in);
 size_t sparse24_meta_offset(int d_out, int d_in);

@@ -111,3 +111,15 @@ def test_binding_refuses_tensors_that_the_call_would_misread(monkeypatch):
         with pytest.raises(B.SblError) as e:
             a(bad, torch.float32, 32)
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("status,kw", [
+    (1, dict(flags=2)), (1, dict(Xq=None)), (1, dict(amax=None)), (1, dict(Wq=None)), (1, dict(wmax=None)),
+    (1, dict(Y=None)), (2, dict(T=-1)), (2, dict(d_in=24)), (2, dict(d_in=0)), (2, dict(d_in=131072)),
+    (2, dict(d_out=12)), (2, dict(d_out=-8)), (3, dict(Xq=AL + 8)), (3, dict(wmax=AL + 4)), (3, dict(Y=AL + 2)),
+    (0, dict(T=0)), (0, dict(d_out=0)),
+])
+def test_forward_w8a8_refuses(cl, status, kw):
+    a = dict(Xq=AL, amax=AL, Wq=AL, wmax=AL, T=4, d_in=32, d_out=16, flags=0, Y=AL)
+    a.update(kw)
+    assert cl.sbl_forward_w8a8(*a.values(), None) == status
