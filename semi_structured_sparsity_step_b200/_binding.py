@@ -128,7 +128,9 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without building a Stream object for every call
+        # (0.3 us against 3.4 us, of 4 us for a whole launch)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -140,27 +142,24 @@ def _call(name, *args):
         raise SblError(name, st)
 
 
-class _Args:
-    """Checks the tensor arguments of one call and gives their device pointers.
+def _args(fn):
+    """Checker of the tensor arguments of one call, which gives their device pointers.
 
     A tensor must be on the current device (where the call is launched),
     contiguous, of the named type and hold at least as many elements as the
     call touches; anything else raises SBL_ERR_INVALID_ARG before the library
     is entered.  None and raw pointers (ints) pass through."""
+    import torch
+    dev = torch.cuda.current_device()
 
-    __slots__ = ("fn", "dev")
-
-    def __init__(self, fn):
-        import torch
-        self.fn = fn
-        self.dev = torch.cuda.current_device()
-
-    def __call__(self, x, dtype, numel):
-        if x is None or isinstance(x, int):
+    def arg(x, dtype, numel):
+        if x is None or x.__class__ is int:
             return x
-        if x.dtype != dtype or x.numel() < numel or x.get_device() != self.dev or not x.is_contiguous():
-            raise SblError(self.fn, 1)
-        return x.data_ptr()
+        if x.dtype is dtype and x.numel() >= numel and x.get_device() == dev and x.is_contiguous():
+            return x.data_ptr()
+        raise SblError(fn, 1)
+
+    return arg
 
 
 def sbl_status_string(status: int) -> str:
@@ -221,7 +220,7 @@ def sbl_grad_group_workspace_bytes(count: int) -> int:
 def _grad_tensors(fn, tensors):
     """tensors: sequence of (g, out_or_None, n, bf16) -> (checker, descriptor array, count)."""
     import torch
-    a = _Args(fn)
+    a = _args(fn)
     words = []
     for g, out, n, bf16 in tensors:
         dt = torch.bfloat16 if bf16 else torch.float32
@@ -290,7 +289,7 @@ def _gate_count(gate, gate_period, T):
 def sbl_block_norm(Y, H, g_post, gate, gate_period, res_scale, g_pre, eps, T, d, flags, H_out, Xn, Xq, amax, rstd,
                    stream=None) -> None:
     import torch
-    a = _Args("sbl_block_norm")
+    a = _args("sbl_block_norm")
     f32, bf16 = torch.float32, torch.bfloat16
     yt, ht, n = bf16 if flags & SBL_BLOCK_Y_BF16 else f32, f32 if flags & SBL_BLOCK_H_F32 else bf16, T * d
     _call("sbl_block_norm", a(Y, yt, n), a(H, ht, n), a(g_post, bf16, d),
@@ -307,7 +306,7 @@ def sbl_block_norm_backward(dXn, dH_out, Y, H_out, g_post, gate, gate_period, re
                             dH, dg_post, dg_pre, dgate, accumulate, workspace, workspace_bytes, stream=None) -> None:
     """dXn: sequence of 1 to 3 gradients of xn (one per product that reads it)."""
     import torch
-    a = _Args("sbl_block_norm_backward")
+    a = _args("sbl_block_norm_backward")
     f32, bf16 = torch.float32, torch.bfloat16
     yt, ht, n = bf16 if flags & SBL_BLOCK_Y_BF16 else f32, f32 if flags & SBL_BLOCK_H_F32 else bf16, T * d
     rows = _gate_count(gate, gate_period, T)
@@ -337,7 +336,7 @@ SBL_W8A8_Y_BF16 = 1
 
 def sbl_forward_w8a8(Xq, amax, Wq, wmax, T, d_in, d_out, flags, Y, stream=None) -> None:
     import torch
-    a = _Args("sbl_forward_w8a8")
+    a = _args("sbl_forward_w8a8")
     f32, i8 = torch.float32, torch.int8
     _call("sbl_forward_w8a8", a(Xq, i8, T * d_in), a(amax, f32, T), a(Wq, i8, d_out * d_in), a(wmax, f32, d_out), T,
           d_in, d_out, flags, a(Y, torch.bfloat16 if flags & SBL_W8A8_Y_BF16 else f32, T * d_out), _stream(stream))

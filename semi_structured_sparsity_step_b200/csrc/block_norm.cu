@@ -13,7 +13,10 @@
 //
 // HBM bound: one read of y and h, one write of h', xn and the codes.  A row lives in registers
 // (VPT vectors of 4 columns per thread, TPR threads per row) between its three reductions (sum of
-// y^2, sum of h'^2, max |xn|); gains and gate rows come from L1/L2.
+// y^2, sum of h'^2, max |xn|); gains and gate rows come from L1/L2.  The reductions are a chain of
+// barriers, so the rows to come are kept on their way: each group of TPR threads has a ring of
+// staged rows in shared memory, filled by bulk copies, and refills a slot once its row is in
+// registers.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -40,6 +43,8 @@ struct BlockNormArgs {
   float* rstd;    // [2, T]; may be NULL
   float res_scale, eps;
   int period, T, nv;  // nv = d / 4
+  int depth;          // rows of the ring
+  uint32_t* err;
 };
 
 template <int TPR, int THREADS, typename V>
@@ -50,11 +55,13 @@ __device__ __forceinline__ V bn_reduce(V x, V* scratch, int rib, bool is_max) {
     const V y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
     x = is_max ? (x > y ? x : y) : x + y;
   }
-  if constexpr (WPR > 1) {
+  if constexpr (WPR == 1) {
+    __syncwarp();
+  } else {
     // each reduction of a row has its own scratch, and the barriers of the row's other
     // reductions keep a fast warp from overwriting it before every warp has read it
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
-    __syncthreads();
+    lane_sync<TPR, THREADS>(rib);
     x = scratch[rib * WPR];
 #pragma unroll
     for (int w = 1; w < WPR; ++w) {
@@ -79,24 +86,51 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
   const int tr = threadIdx.x % TPR;
   const double d = static_cast<double>(a.nv) * 4.0;
   const double eps = static_cast<double>(a.eps);
+  extern __shared__ __align__(128) uint8_t ring[];
+  const uint32_t y_bytes = static_cast<uint32_t>(a.nv) * (YB ? 8u : 16u);
+  const uint32_t h_bytes = static_cast<uint32_t>(a.nv) * (HF ? 16u : 8u);
+  const uint32_t slot_bytes = y_bytes + h_bytes;
+  uint8_t* slots = ring + static_cast<size_t>(rib) * a.depth * slot_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + static_cast<size_t>(RPB) * a.depth * slot_bytes) + rib * a.depth;
+  const long long stride = static_cast<long long>(gridDim.x) * RPB;
+  __shared__ int s_abort;
+  if (tr == 0) {
+    for (int i = 0; i < a.depth; ++i) mbar_init(&bars[i], 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  auto request = [&](long long row, int slot) {
+    uint8_t* dst = slots + static_cast<size_t>(slot) * slot_bytes;
+    mbar_arrive_expect_tx(&bars[slot], slot_bytes);
+    bulk_load(dst, static_cast<const uint8_t*>(a.Y) + row * y_bytes, y_bytes, &bars[slot]);
+    bulk_load(dst + y_bytes, static_cast<const uint8_t*>(a.H) + row * h_bytes, h_bytes, &bars[slot]);
+  };
+  __syncthreads();
   pdl::wait();
+  const long long row0 = static_cast<long long>(blockIdx.x) * RPB + rib;
+  if (tr == 0)
+    for (int i = 0; i < a.depth; ++i)
+      if (row0 + i * stride < a.T) request(row0 + i * stride, i);
 
-  for (long long base = static_cast<long long>(blockIdx.x) * RPB; base < a.T;
-       base += static_cast<long long>(gridDim.x) * RPB) {
+  RingPos pos;
+  for (long long base = static_cast<long long>(blockIdx.x) * RPB; base < a.T; base += stride) {
     const long long row = base + rib;
     const bool active = row < a.T;
     const int rc = static_cast<int>(active ? row : static_cast<long long>(a.T) - 1);
     const long long at = static_cast<long long>(rc) * a.nv;
-    float y[VPT][4], h[VPT][4];
+    const uint8_t* staged = slots + static_cast<size_t>(pos.slot) * slot_bytes;
+    const int slot = pos.slot;
+    if (active) mbar_wait(&bars[slot], pos.parity, &s_abort, a.err);
+    pos.next(a.depth);
+    float y[VPT][4];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = tr + k * TPR;
-      if (i < a.nv) {
-        load4<YB>(a.Y, at + i, y[k]);
-        load4<!HF>(a.H, at + i, h[k]);
+      if (active && i < a.nv) {
+        staged4<YB>(staged, i, y[k]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = h[k][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) y[k][j] = 0.0f;
       }
     }
     float r1 = 1.0f;
@@ -135,21 +169,32 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = tr + k * TPR;
+      if (active && i < a.nv) {
+        float h[4];
+        staged4<!HF>(staged + y_bytes, i, h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[k][j] = __fadd_rn(__fmul_rn(a.res_scale, h[k][j]), y[k][j]);
-        if constexpr (!HF) h[k][j] = __bfloat162float(__float2bfloat16_rn(h[k][j]));
-      }
-      if (i < a.nv) {
-        if (active) store4<!HF>(a.H_out, at + i, h[k]);
+        for (int j = 0; j < 4; ++j) h[j] = __fadd_rn(__fmul_rn(a.res_scale, h[j]), y[k][j]);
+        if constexpr (HF) {
+          static_cast<float4*>(a.H_out)[at + i] = make_float4(h[0], h[1], h[2], h[3]);
+        } else {
+          const uint2 w = pack4(h);
+          static_cast<uint2*>(a.H_out)[at + i] = w;
+          unpack4(w, h);
+        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const double v = static_cast<double>(h[k][j]);
+          y[k][j] = h[j];  // the row is h' from here on
+          const double v = static_cast<double>(h[j]);
           ss = fma(v, v, ss);
         }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[k][j] = 0.0f;
       }
     }
     ss = bn_reduce<TPR, THREADS, double>(ss, s_h, rib, false);
+    // every thread of the group has its columns in registers
+    if (tr == 0 && row + a.depth * stride < a.T) request(row + a.depth * stride, slot);
     const float r2 = bn_rstd(ss, d, eps);
     uint32_t mx = 0u;
     uint2 xn[VPT];
@@ -159,8 +204,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
       float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
       if (i < a.nv) unpack4(__ldg(a.g_pre + i), g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) h[k][j] = __fmul_rn(__fmul_rn(h[k][j], r2), g[j]);
-      xn[k] = pack4(h[k]);
+      for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(__fmul_rn(y[k][j], r2), g[j]);
+      xn[k] = pack4(y[k]);
       if (i < a.nv) {
         mx = __vmaxu2(mx, __vmaxu2(xn[k].x & 0x7FFF7FFFu, xn[k].y & 0x7FFF7FFFu));
         if (active && a.Xn != nullptr) a.Xn[at + i] = xn[k];
@@ -198,30 +243,53 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
   }
 }
 
+constexpr int kBnMaxDepth = 4;
+
 template <int TPR, int VPT, bool YB, bool HF>
-cudaError_t run(const BlockNormArgs& a, int blocks_per_sm, cudaStream_t stream, int num_sms) {
+cudaError_t run(BlockNormArgs a, int blocks_per_sm, cudaStream_t stream, int num_sms) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
   constexpr int RPB = THREADS / TPR;
   long long blocks = (static_cast<long long>(a.T) + RPB - 1) / RPB;
   const long long cap = static_cast<long long>(num_sms) * blocks_per_sm;
   if (blocks > cap) blocks = cap;
-  return pdl::launch(block_norm_kernel<TPR, VPT, YB, HF>, static_cast<int>(blocks), THREADS, 0, 1, stream, a);
+  // as many rows ahead as the block's share of shared memory holds, and no more than it has rows
+  const int slot = a.nv * ((YB ? 8 : 16) + (HF ? 16 : 8)) * RPB;
+  const int budget = 220 * 1024 / blocks_per_sm - 1024;
+  const long long rows = (static_cast<long long>(a.T) + blocks * RPB - 1) / (blocks * RPB);
+  a.depth = budget / slot < kBnMaxDepth ? budget / slot : kBnMaxDepth;
+  if (a.depth > rows) a.depth = static_cast<int>(rows);
+  if (a.depth < 1) a.depth = 1;
+  const int smem = a.depth * slot + RPB * a.depth * 8;
+  auto kern = block_norm_kernel<TPR, VPT, YB, HF>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024);
+  if (e != cudaSuccess) return e;
+  return pdl::launch(kern, static_cast<int>(blocks), THREADS, smem, 1, stream, a);
 }
 
 template <bool YB, bool HF>
 cudaError_t dispatch(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
-  if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 8, stream, num_sms);
-  if (a.nv <= 64 * 2) return run<64, 2, YB, HF>(a, 8, stream, num_sms);
-  if (a.nv <= 128 * 2) return run<128, 2, YB, HF>(a, 8, stream, num_sms);
-  if (a.nv <= 256 * 2) return run<256, 2, YB, HF>(a, 8, stream, num_sms);
-  if (a.nv <= 512 * 2) return run<512, 2, YB, HF>(a, 4, stream, num_sms);
-  if (a.nv <= 512 * 4) return run<512, 4, YB, HF>(a, 4, stream, num_sms);
-  return run<512, 8, YB, HF>(a, 4, stream, num_sms);
+  if (a.T > 4 * num_sms) {
+    // many rows: 32 columns per thread
+    if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 4, stream, num_sms);
+    if (a.nv <= 32 * 4) return run<32, 4, YB, HF>(a, 4, stream, num_sms);
+    if (a.nv <= 32 * 8) return run<32, 8, YB, HF>(a, 2, stream, num_sms);
+    if (a.nv <= 64 * 8) return run<64, 8, YB, HF>(a, 2, stream, num_sms);
+    if (a.nv <= 128 * 8) return run<128, 8, YB, HF>(a, 2, stream, num_sms);
+    if (a.nv <= 256 * 8) return run<256, 8, YB, HF>(a, 2, stream, num_sms);
+    return run<512, 8, YB, HF>(a, 1, stream, num_sms);
+  }
+  if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 64 * 2) return run<64, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 128 * 2) return run<128, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 256 * 2) return run<256, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 512 * 2) return run<512, 2, YB, HF>(a, 2, stream, num_sms);
+  if (a.nv <= 512 * 4) return run<512, 4, YB, HF>(a, 1, stream, num_sms);
+  return run<512, 8, YB, HF>(a, 1, stream, num_sms);
 }
 
 }  // namespace
 
-cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms) {
+cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms, uint32_t* err) {
   if (p.T == 0) return cudaSuccess;
   BlockNormArgs a{};
   a.Y = p.Y;
@@ -239,6 +307,7 @@ cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int nu
   a.period = p.gate_period;
   a.T = p.T;
   a.nv = p.d / 4;
+  a.err = err;
   if (p.y_bf16) return p.h_f32 ? dispatch<true, true>(a, stream, num_sms) : dispatch<true, false>(a, stream, num_sms);
   return p.h_f32 ? dispatch<false, true>(a, stream, num_sms) : dispatch<false, false>(a, stream, num_sms);
 }

@@ -1,10 +1,13 @@
-// block_norm.cuh -- what the block norm's forward and backward kernels share: loads and stores
-// of 4 neighbouring columns in either type, and the dependent launch.
+// block_norm.cuh -- what the block norm's forward and backward kernels share: 4 neighbouring
+// columns in either type, the ring of rows that bulk copies keep ahead of the arithmetic, and the
+// dependent launch.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
+
+#include "sbl_device.cuh"
 
 namespace sbl {
 
@@ -22,14 +25,13 @@ __device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// Columns 4 i .. 4 i + 3 of a bf16 (kBf16) or fp32 array (plain loads: the
-// output may be the input's own buffer).
+// Columns 4 i .. 4 i + 3 of a staged row, bf16 (kBf16) or fp32.
 template <bool kBf16>
-__device__ __forceinline__ void load4(const void* p, long long i, float (&x)[4]) {
+__device__ __forceinline__ void staged4(const uint8_t* row, int i, float (&x)[4]) {
   if constexpr (kBf16) {
-    unpack4(static_cast<const uint2*>(p)[i], x);
+    unpack4(reinterpret_cast<const uint2*>(row)[i], x);
   } else {
-    const float4 v = static_cast<const float4*>(p)[i];
+    const float4 v = reinterpret_cast<const float4*>(row)[i];
     x[0] = v.x;
     x[1] = v.y;
     x[2] = v.z;
@@ -44,6 +46,40 @@ __device__ __forceinline__ void store4(void* p, long long i, const float (&x)[4]
   } else {
     static_cast<float4*>(p)[i] = make_float4(x[0], x[1], x[2], x[3]);
   }
+}
+
+// Bulk copy of `bytes` (a multiple of 16) from global memory to shared memory, both 16-byte
+// aligned; completes on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// Position in a ring of `depth` slots, with the parity of the barrier phase that fills it.
+struct RingPos {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int depth) {
+    if (++slot == depth) {
+      slot = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Barrier of the TPR threads of row lane `rib` (a warp of its own, or one named barrier per lane), so
+// the lanes of a block keep their own pace.  A slot may be refilled behind it: every value read from
+// the slot has gone into the sums that the threads bring to the barrier.
+template <int TPR, int THREADS>
+__device__ __forceinline__ void lane_sync(int rib) {
+  if constexpr (TPR == 32)
+    __syncwarp();
+  else if constexpr (TPR == THREADS)
+    __syncthreads();
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(rib + 1), "n"(TPR) : "memory");
 }
 
 // Programmatic dependent launch: a kernel may be set up while the previous one of its stream

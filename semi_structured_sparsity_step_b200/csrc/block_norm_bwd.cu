@@ -14,11 +14,13 @@
 // HBM bound: one read of each dX, dH, y and h', one write of dy and dh.  TPR threads share a row,
 // 8 columns each (2048 columns per block; wider rows go to a cluster of CS blocks that exchange the
 // three sums through distributed shared memory).  A thread keeps its columns for all its rows, so
-// the column sums stay in registers; the next row's loads are in flight while the current row
-// waits for its sums.  Column sums leave as one partial row per block (dgate: per segment of rows
+// the column sums stay in registers.  The rows to come are staged in a ring in shared memory by
+// bulk copies, one ring per row lane; a slot is refilled once its row's sums have met.  Column sums leave as one partial row per block (dgate: per segment of rows
 // with one gate row), and a second launch adds the partial rows in a fixed order: no atomics.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "block_norm.cuh"
@@ -35,7 +37,7 @@ constexpr int kBbMaxSms = 160;       // sizes the workspace
 constexpr int kBbWaves = 4;          // segments per row lane at most
 
 struct BwdArgs {
-  const float4* dXn[3];
+  const float* dXn[3];
   const void* dH_in;     // may be NULL (zero)
   const void* Y;
   const void* H;         // h'
@@ -53,66 +55,9 @@ struct BwdArgs {
   float res_scale;
   int T, nv, vecs_per_cta;
   int period, seg_rows, segs_per_group, segs;  // tokens per gate row, rows per segment
+  int depth, slot_bytes; // rows of the ring, bytes of a staged row (at most)
+  uint32_t* err;
 };
-
-template <bool kBf16>
-struct Raw4 {
-  uint2 v;
-  __device__ __forceinline__ void load(const void* p, long long i) { v = static_cast<const uint2*>(p)[i]; }
-  __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
-  __device__ __forceinline__ void get(float (&x)[4]) const { unpack4(v, x); }
-};
-template <>
-struct Raw4<false> {
-  float4 v;
-  __device__ __forceinline__ void load(const void* p, long long i) { v = static_cast<const float4*>(p)[i]; }
-  __device__ __forceinline__ void zero() { v = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
-  __device__ __forceinline__ void get(float (&x)[4]) const {
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  }
-};
-
-template <bool YB, bool HF>
-struct RawRow {
-  Raw4<YB> y[kBbVpt];
-  Raw4<!HF> h[kBbVpt], dh[kBbVpt];
-  float4 dx[3][kBbVpt];
-  uint2 gate[kBbVpt];
-  float r1, r2;
-};
-
-template <int TPR, bool YB, bool HF>
-__device__ __forceinline__ void load_row(RawRow<YB, HF>& r, const BwdArgs& a, int row, bool active, int v0, int v1) {
-  r.r1 = r.r2 = 0.0f;
-  if (active) {
-    r.r1 = __ldg(a.rstd + row);
-    r.r2 = __ldg(a.rstd + a.T + row);
-  }
-  const long long at = static_cast<long long>(row) * a.nv;
-  const long long gat = a.gate != nullptr && active ? static_cast<long long>(row / a.period) * a.nv : 0;
-#pragma unroll
-  for (int k = 0; k < kBbVpt; ++k) {
-    const int i = v0 + k * TPR;
-    r.y[k].zero();
-    r.h[k].zero();
-    r.dh[k].zero();
-    r.gate[k] = make_uint2(0x3F803F80u, 0x3F803F80u);  // 1.0
-#pragma unroll
-    for (int q = 0; q < 3; ++q) r.dx[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (active && i < v1) {
-      r.y[k].load(a.Y, at + i);
-      r.h[k].load(a.H, at + i);
-      if (a.dH_in != nullptr) r.dh[k].load(a.dH_in, at + i);
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        if (q < a.readers) r.dx[q][k] = __ldg(a.dXn[q] + at + i);
-      if (a.gate != nullptr) r.gate[k] = __ldg(a.gate + gat + i);
-    }
-  }
-}
 
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
@@ -126,7 +71,6 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
   constexpr int WPR = TPR / 32;
   constexpr int SLOTS = CS > 1 ? CS * 8 : 8;
   __shared__ float4 s_sum[2][SLOTS];
-  __shared__ float4 s_col[kBbThreads * kBbVpt];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rib = threadIdx.x / TPR;
   const int tr = threadIdx.x % TPR;
@@ -137,6 +81,40 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
   const int v1 = min(a.nv, (rank + 1) * a.vecs_per_cta);
   const bool post = a.g_post != nullptr;
   const float inv_d = 1.0f / (4.0f * static_cast<float>(a.nv));
+  // one staged row: y, h', dH (if given), the readers' gradients, the gate row (if given)
+  const int cols = (v1 - rank * a.vecs_per_cta) * 4;
+  const uint32_t b16 = static_cast<uint32_t>(cols > 0 ? cols : 0) * 2u, b32 = 2u * b16;
+  const uint32_t y_bytes = YB ? b16 : b32, h_bytes = HF ? b32 : b16;
+  const uint32_t off_dh = y_bytes + h_bytes;
+  const uint32_t off_dx = off_dh + (a.dH_in != nullptr ? h_bytes : 0u);
+  const uint32_t off_gate = off_dx + static_cast<uint32_t>(a.readers) * b32;
+  const uint32_t row_bytes = off_gate + (a.gate != nullptr ? b16 : 0u);
+  extern __shared__ __align__(128) uint8_t ring[];
+  uint8_t* slots = ring + static_cast<size_t>(rib) * a.depth * a.slot_bytes;
+  uint64_t* bars =
+      reinterpret_cast<uint64_t*>(ring + static_cast<size_t>(RPB) * a.depth * a.slot_bytes) + rib * a.depth;
+  __shared__ int s_abort;
+  if (tr == 0) {
+    for (int i = 0; i < a.depth; ++i) mbar_init(&bars[i], 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  auto request = [&](int row, int slot) {
+    uint8_t* dst = slots + static_cast<size_t>(slot) * a.slot_bytes;
+    uint64_t* bar = &bars[slot];
+    const long long at = static_cast<long long>(row) * a.nv * 4 + rank * a.vecs_per_cta * 4;
+    mbar_arrive_expect_tx(bar, row_bytes);
+    bulk_load(dst, static_cast<const uint8_t*>(a.Y) + at * (YB ? 2 : 4), y_bytes, bar);
+    bulk_load(dst + y_bytes, static_cast<const uint8_t*>(a.H) + at * (HF ? 4 : 2), h_bytes, bar);
+    if (a.dH_in != nullptr)
+      bulk_load(dst + off_dh, static_cast<const uint8_t*>(a.dH_in) + at * (HF ? 4 : 2), h_bytes, bar);
+    for (int q = 0; q < a.readers; ++q) bulk_load(dst + off_dx + q * b32, a.dXn[q] + at, b32, bar);
+    if (a.gate != nullptr) {
+      const long long gat = static_cast<long long>(row / a.period) * a.nv * 4 + rank * a.vecs_per_cta * 4;
+      bulk_load(dst + off_gate, reinterpret_cast<const uint8_t*>(a.gate) + gat * 2, b16, bar);
+    }
+  };
+  __syncthreads();
   if constexpr (CS > 1) pair::cluster_sync();  // every block of the cluster is there
   pdl::wait();
 
@@ -157,65 +135,96 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
   // Every row lane walks its segments, seg_rows steps each (steps past the segment's rows are
   // inactive), so all lanes of a block or cluster take the same number of steps and barriers.
   const int rounds = (a.segs + units - 1) / units;
-  auto locate = [&](int seg, int step, int& row) {
-    if (seg >= a.segs) {
-      row = 0;
-      return false;
-    }
-    const int group = seg / a.segs_per_group;
-    const long long first = static_cast<long long>(group) * a.period;
-    const long long in_group = static_cast<long long>(seg - group * a.segs_per_group) * a.seg_rows + step;
-    row = static_cast<int>(min(first + in_group, static_cast<long long>(a.T)));
-    return in_group < a.period && first + in_group < a.T;
+  struct Walk {
+    int seg, step, row, rows;  // rows: how many of the segment's steps are active
   };
+  auto enter = [&](Walk& w) {
+    w.step = 0;
+    w.row = w.rows = 0;
+    if (w.seg < a.segs) {
+      const int group = w.seg / a.segs_per_group;
+      const long long in_group = static_cast<long long>(w.seg - group * a.segs_per_group) * a.seg_rows;
+      const long long first = static_cast<long long>(group) * a.period + in_group;
+      const long long left = min(static_cast<long long>(a.period) - in_group, static_cast<long long>(a.T) - first);
+      w.row = static_cast<int>(min(first, static_cast<long long>(a.T)));
+      w.rows = static_cast<int>(max(0ll, min(left, static_cast<long long>(a.seg_rows))));
+    }
+  };
+  // The requests run ahead of the arithmetic through the same sequence of active rows.
+  Walk ahead{unit, 0, 0, 0}, w{unit, 0, 0, 0};
+  enter(ahead);
+  enter(w);
+  RingPos fill, pos;
+  auto request_next = [&]() {
+    while (ahead.step >= ahead.rows) {
+      if (ahead.seg >= a.segs) return;
+      ahead.seg += units;
+      enter(ahead);
+    }
+    request(ahead.row + ahead.step, fill.slot);
+    ++ahead.step;
+    fill.next(a.depth);
+  };
+  if (tr == 0 && cols > 0)
+    for (int i = 0; i < a.depth; ++i) request_next();
 
-  RawRow<YB, HF> raw;
-  int row, buf = 0;
-  bool active = locate(unit, 0, row);
-  load_row<TPR>(raw, a, row, active, v0, v1);
+  int buf = 0;
   for (int rd = 0; rd < rounds; ++rd) {
-    const int seg = rd * units + unit;
+    const int seg = w.seg;
     for (int step = 0; step < a.seg_rows; ++step) {
-      const float r1 = raw.r1, r2 = raw.r2;
+      const bool cur_active = step < w.rows;
+      const int cur_row = w.row + step;
+      float cur_r1 = 0.0f, cur_r2 = 0.0f;
+      if (cur_active) {
+        cur_r1 = __ldg(a.rstd + cur_row);
+        cur_r2 = __ldg(a.rstd + a.T + cur_row);
+      }
+      const uint8_t* staged = slots + static_cast<size_t>(pos.slot) * a.slot_bytes;
+      if (cur_active && cols > 0) {
+        mbar_wait(&bars[pos.slot], pos.parity, &s_abort, a.err);
+        pos.next(a.depth);
+      }
       float t[kBbVpt][4], xh[kBbVpt][4], dhin[kBbVpt][4], yh[kBbVpt][4];
       uint2 gt[kBbVpt];
       float s2 = 0.0f, sa = 0.0f, sb = 0.0f;
 #pragma unroll
       for (int k = 0; k < kBbVpt; ++k) {
+        const int i = tr + k * TPR;
+        gt[k] = make_uint2(0x3F803F80u, 0x3F803F80u);  // 1.0
+        float dx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xh[k][j] = dhin[k][j] = yh[k][j] = dx[j] = 0.0f;
+        if (cur_active && v0 + k * TPR < v1) {
+          staged4<YB>(staged, i, yh[k]);
+          staged4<!HF>(staged + y_bytes, i, xh[k]);
+          if (a.dH_in != nullptr) staged4<!HF>(staged + off_dh, i, dhin[k]);
+          staged4<false>(staged + off_dx, i, dx);
+          for (int q = 1; q < a.readers; ++q) {
+            float more[4];
+            staged4<false>(staged + off_dx + q * b32, i, more);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dx[j] += more[j];
+          }
+          if (a.gate != nullptr) gt[k] = reinterpret_cast<const uint2*>(staged + off_gate)[i];
+        }
         float g[4], gp[4], gg[4];
         unpack4(gpre[k], g);
         unpack4(gpost[k], gp);
-        gt[k] = raw.gate[k];
         unpack4(gt[k], gg);
-        raw.h[k].get(xh[k]);
-        raw.dh[k].get(dhin[k]);
-        raw.y[k].get(yh[k]);
-        const float dx[4] = {raw.dx[0][k].x + raw.dx[1][k].x + raw.dx[2][k].x,
-                             raw.dx[0][k].y + raw.dx[1][k].y + raw.dx[2][k].y,
-                             raw.dx[0][k].z + raw.dx[1][k].z + raw.dx[2][k].z,
-                             raw.dx[0][k].w + raw.dx[1][k].w + raw.dx[2][k].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          xh[k][j] *= r2;
+          xh[k][j] *= cur_r2;
           acc_pre[k][j] = fmaf(dx[j], xh[k][j], acc_pre[k][j]);
           t[k][j] = dx[j] * g[j];
           s2 = fmaf(t[k][j], xh[k][j], s2);
           if (post) {
-            yh[k][j] *= r1;
-            const float w = gg[j] * gp[j] * yh[k][j];
-            sa = fmaf(w, fmaf(r2, t[k][j], dhin[k][j]), sa);
-            sb = fmaf(w, xh[k][j], sb);
+            yh[k][j] *= cur_r1;
+            const float wt = gg[j] * gp[j] * yh[k][j];
+            sa = fmaf(wt, fmaf(cur_r2, t[k][j], dhin[k][j]), sa);
+            sb = fmaf(wt, xh[k][j], sb);
           }
         }
       }
-      const int cur_row = row;
-      const bool cur_active = active;
-      if (step + 1 < a.seg_rows)
-        active = locate(seg, step + 1, row);
-      else
-        active = locate(seg + units, 0, row);
-      load_row<TPR>(raw, a, row, active, v0, v1);
-
       s2 = warp_sum(s2);
       if (post) {
         sa = warp_sum(sa);
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
         }
       } else if constexpr (WPR > 1) {
         if (lane == 0) s_sum[buf][warp] = make_float4(s2, sa, sb, 0.0f);
-        __syncthreads();
+        lane_sync<TPR, kBbThreads>(rib);
         s2 = sa = sb = 0.0f;
 #pragma unroll
         for (int w = 0; w < WPR; ++w) {
@@ -253,10 +262,14 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
           sa += v.y;
           sb += v.z;
         }
+      } else {
+        __syncwarp();
       }
+      // every thread of the row lane is past its reads of the slot
+      if (tr == 0 && cur_active && cols > 0) request_next();
       buf ^= 1;  // two buffers: a warp can be at most one barrier ahead of another's reads
       const float c2 = s2 * inv_d;
-      const float c1 = fmaf(-r2 * c2, sb, sa) * inv_d;
+      const float c1 = fmaf(-cur_r2 * c2, sb, sa) * inv_d;
       const long long at = static_cast<long long>(cur_row) * a.nv;
 #pragma unroll
       for (int k = 0; k < kBbVpt; ++k) {
@@ -266,13 +279,13 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
         unpack4(gt[k], gg);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float d = fmaf(r2, fmaf(-xh[k][j], c2, t[k][j]), dhin[k][j]);
+          const float d = fmaf(cur_r2, fmaf(-xh[k][j], c2, t[k][j]), dhin[k][j]);
           dh[j] = a.res_scale * d;
           acc_gate[k][j] = fmaf(d, yh[k][j] * gp[j], acc_gate[k][j]);
           const float du = gg[j] * d;
           if (post) {
             acc_post[k][j] = fmaf(du, yh[k][j], acc_post[k][j]);
-            dy[j] = r1 * fmaf(-yh[k][j], c1, du * gp[j]);
+            dy[j] = cur_r1 * fmaf(-yh[k][j], c1, du * gp[j]);
           } else {
             dy[j] = du;
           }
@@ -283,6 +296,8 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
         }
       }
     }
+    w.seg += units;
+    enter(w);
     if (a.gate_out != nullptr && seg < a.segs) {
 #pragma unroll
       for (int k = 0; k < kBbVpt; ++k) {
@@ -302,7 +317,9 @@ __global__ void __launch_bounds__(kBbThreads, kBbBlocksPerSm) block_norm_bwd_ker
     }
   }
 
-  // the block's row lanes meet in shared memory: one partial row per block
+  // the block's row lanes meet in shared memory (the ring's, every staged row is consumed): one
+  // partial row per block
+  float4* s_col = reinterpret_cast<float4*>(ring);
   auto leave = [&](const float (&acc)[kBbVpt][4], float4* part) {
     __syncthreads();
 #pragma unroll
@@ -395,13 +412,60 @@ int max_units(int d, int sms) {
   return kBbBlocksPerSm * sms / s.cs * (kBbThreads / s.tpr);
 }
 
+constexpr int kBbRingBytes = 104 * 1024;  // per block, two blocks per SM
+constexpr int kBbMaxDepth = 4;
+constexpr int kBbColBytes = kBbThreads * kBbVpt * 16;  // the row lanes' column sums, at the end
+
+template <int TPR, int CS, bool YB, bool HF>
+cudaError_t run_typed(BwdArgs a, int grid, cudaStream_t stream) {
+  constexpr int RPB = kBbThreads / TPR;
+  a.slot_bytes = a.vecs_per_cta * 4 *
+                 ((YB ? 2 : 4) + (HF ? 4 : 2) * (a.dH_in != nullptr ? 2 : 1) + 4 * a.readers + (a.gate != nullptr ? 2 : 0));
+  a.depth = kBbRingBytes / (RPB * a.slot_bytes);
+  if (a.depth > kBbMaxDepth) a.depth = kBbMaxDepth;
+  if (a.depth < 1) a.depth = 1;
+  int smem = RPB * a.depth * (a.slot_bytes + 8);
+  if (smem < kBbColBytes) smem = kBbColBytes;
+  auto kern = block_norm_bwd_kernel<TPR, CS, YB, HF>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBbRingBytes + 1024);
+  if (e != cudaSuccess) return e;
+  return pdl::launch(kern, grid, kBbThreads, smem, CS, stream, a);
+}
+
+// How many clusters of CS blocks are resident at once: fewer than the SMs alone would hold, as a
+// cluster stays within one group of SMs.  Asked once per device for the widest staged row.
+template <int CS>
+int resident_clusters(int num_sms) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return num_sms / CS;
+  int n = cached[dev].load();
+  if (n == 0) {
+    auto kern = block_norm_bwd_kernel<256, CS, false, true>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CS);
+    cfg.blockDim = dim3(kBbThreads);
+    cfg.dynamicSmemBytes = kBbRingBytes + 1024;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBbRingBytes + 1024) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+      n = num_sms / CS;
+    if (n > kBbBlocksPerSm * num_sms / CS) n = kBbBlocksPerSm * num_sms / CS;
+    cached[dev].store(n);
+  }
+  return n;
+}
+
 template <int TPR, int CS>
 cudaError_t run(const BwdArgs& a, bool yb, bool hf, int grid, cudaStream_t stream) {
-  if (yb)
-    return hf ? pdl::launch(block_norm_bwd_kernel<TPR, CS, true, true>, grid, kBbThreads, 0, CS, stream, a)
-              : pdl::launch(block_norm_bwd_kernel<TPR, CS, true, false>, grid, kBbThreads, 0, CS, stream, a);
-  return hf ? pdl::launch(block_norm_bwd_kernel<TPR, CS, false, true>, grid, kBbThreads, 0, CS, stream, a)
-            : pdl::launch(block_norm_bwd_kernel<TPR, CS, false, false>, grid, kBbThreads, 0, CS, stream, a);
+  if (yb) return hf ? run_typed<TPR, CS, true, true>(a, grid, stream) : run_typed<TPR, CS, true, false>(a, grid, stream);
+  return hf ? run_typed<TPR, CS, false, true>(a, grid, stream) : run_typed<TPR, CS, false, false>(a, grid, stream);
 }
 
 }  // namespace
@@ -413,7 +477,7 @@ size_t block_norm_bwd_workspace_bytes(int d) {
   return (2 + kBbWaves) * units * static_cast<size_t>(d) * sizeof(float);
 }
 
-cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream, int num_sms) {
+cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream, int num_sms, uint32_t* err) {
   const int nv = p.d / 4;
   cudaError_t e = cudaSuccess;
   if (p.T == 0) {
@@ -426,7 +490,10 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream,
   const Shape sh = shape_of(p.d);
   const int rpb = kBbThreads / sh.tpr;
   if (num_sms > kBbMaxSms) num_sms = kBbMaxSms;
-  const int units_max = max_units(p.d, num_sms);
+  int units_max = max_units(p.d, num_sms);
+  if (sh.cs == 2) units_max = std::min(units_max, resident_clusters<2>(num_sms));
+  if (sh.cs == 4) units_max = std::min(units_max, resident_clusters<4>(num_sms));
+  if (sh.cs == 8) units_max = std::min(units_max, resident_clusters<8>(num_sms));
   // Cut each group of tokens that share a gate row into segs_per_group segments: the choice with
   // the fewest steps on the busiest row lane, a segment's end counted as half a step.
   const bool gated = p.gate != nullptr;
@@ -449,7 +516,7 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream,
     }
   }
   BwdArgs a{};
-  for (int q = 0; q < p.readers; ++q) a.dXn[q] = reinterpret_cast<const float4*>(p.dXn[q]);
+  for (int q = 0; q < p.readers; ++q) a.dXn[q] = p.dXn[q];
   a.readers = p.readers;
   a.dH_in = p.dH_out;
   a.Y = p.Y;
@@ -463,7 +530,9 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream,
   a.res_scale = p.res_scale;
   a.T = p.T;
   a.nv = nv;
-  a.vecs_per_cta = sh.cs > 1 ? (nv + sh.cs - 1) / sh.cs : nv;
+  // a multiple of 16 columns, so that every block's slice of a row starts and ends on 16 bytes
+  a.vecs_per_cta = sh.cs > 1 ? (nv / 4 + sh.cs - 1) / sh.cs * 4 : nv;
+  a.err = err;
   a.period = period;
   a.seg_rows = seg_rows;
   a.segs_per_group = per_group;

@@ -188,17 +188,31 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
       const int cols = min(BN, a.T - n0);
       const float sw = o < a.d_out ? __fdiv_rn(a.wmax[o], 127.0f) : 0.0f;
       const uint32_t base = smem_u32(smem) + static_cast<uint32_t>(row) * 4u;
-      for (int c = static_cast<int>(rank); c < cols; c += static_cast<int>(cs)) {
-        int acc = 0;
-        for (uint32_t p = 0; p < cs; ++p) {
-          int v;
-          asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                       : "=r"(v)
-                       : "r"(pair::map_to(base + static_cast<uint32_t>(c) * (kW8Rows * 4u), p))
-                       : "memory");
-          acc += v;
+      // eight columns at a time from every block: up to 64 remote loads in flight
+      for (int c0 = static_cast<int>(rank); c0 < cols; c0 += 8 * static_cast<int>(cs)) {
+        int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (uint32_t p = 0; p < 8; ++p) {
+          if (p >= cs) break;
+          const uint32_t from = pair::map_to(base, p);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int c = c0 + u * static_cast<int>(cs);
+            int v = 0;
+            if (c < cols)
+              asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(from + static_cast<uint32_t>(c) * (kW8Rows * 4u))
+                           : "memory");
+            acc[u] += v;
+          }
         }
-        if (o < a.d_out) w8_store<kBf16>(a.Y, static_cast<long long>(n0 + c) * a.d_out + o, acc, s_sx[c], sw);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int c = c0 + u * static_cast<int>(cs);
+          if (c < cols && o < a.d_out)
+            w8_store<kBf16>(a.Y, static_cast<long long>(n0 + c) * a.d_out + o, acc[u], s_sx[c], sw);
+        }
       }
     }
     __syncwarp();

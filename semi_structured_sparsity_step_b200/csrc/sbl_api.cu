@@ -346,7 +346,7 @@ sbl_status sbl_block_norm(const void* Y, const void* H, const void* g_post, cons
   p.d = d;
   p.y_bf16 = (flags & SBL_BLOCK_Y_BF16) != 0u;
   p.h_f32 = (flags & SBL_BLOCK_H_F32) != 0u;
-  return from_cuda(launch_block_norm(p, static_cast<cudaStream_t>(stream), dev->num_sms));
+  return from_cuda(launch_block_norm(p, static_cast<cudaStream_t>(stream), dev->num_sms, dev->err));
 }
 
 size_t sbl_block_norm_backward_workspace_bytes(int d) {
@@ -400,7 +400,7 @@ sbl_status sbl_block_norm_backward(const float* const* dXn, int readers, const v
   p.y_bf16 = (flags & SBL_BLOCK_Y_BF16) != 0u;
   p.h_f32 = (flags & SBL_BLOCK_H_F32) != 0u;
   p.workspace = workspace;
-  return from_cuda(launch_block_norm_bwd(p, static_cast<cudaStream_t>(stream), dev->num_sms));
+  return from_cuda(launch_block_norm_bwd(p, static_cast<cudaStream_t>(stream), dev->num_sms, dev->err));
 }
 
 sbl_status sbl_forward(const int8_t* Xq, const float* amax, const int8_t* W_eff, const float* gamma, int T,

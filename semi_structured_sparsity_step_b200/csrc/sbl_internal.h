@@ -71,7 +71,7 @@ struct BlockNormDev {
   int gate_period, T, d;
   bool y_bf16, h_f32;
 };
-cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms);
+cudaError_t launch_block_norm(const BlockNormDev& p, cudaStream_t stream, int num_sms, uint32_t* err);
 struct BlockNormBwdDev {
   const float* dXn[3];
   int readers;
@@ -86,7 +86,7 @@ struct BlockNormBwdDev {
 };
 constexpr int kBlockNormMaxWidth = 16384;
 size_t block_norm_bwd_workspace_bytes(int d);
-cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream, int num_sms);
+cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream, int num_sms, uint32_t* err);
 
 // ---- tensor-core GEMMs (gemm_tc.cu)
 // 2-D tensor map of a row-major [rows, inner] uint32 matrix (row stride in

@@ -100,11 +100,12 @@ def test_binding_refuses_tensors_that_the_call_would_misread(monkeypatch):
     import torch
     from semi_structured_sparsity_step_b200 import _binding as B
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    a = B._Args("sbl_block_norm")
+    a = B._args("sbl_block_norm")
     assert a(None, torch.float32, 4) is None and a(AL, torch.float32, 4) == AL
     with pytest.raises(B.SblError):
         a(torch.zeros(4), torch.float32, 4)  # on the host
-    a.dev = -1  # what get_device() gives for the host tensors below
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # what get_device() gives for a host tensor
+    a = B._args("sbl_block_norm")
     x = torch.zeros(4, 8)
     assert a(x, torch.float32, 32) == x.data_ptr()
     for bad in (x.to(torch.bfloat16), x[:, ::2], x[:2], x.t()):
