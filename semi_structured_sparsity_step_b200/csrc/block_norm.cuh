@@ -25,6 +25,38 @@ __device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
+// Two fp32 operations per instruction (sm_100), each rounded as the single one.
+__device__ __forceinline__ float2 splat2(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 mul2(const float2& a, const float2& b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(const float2& a, const float2& b, const float2& c) {
+  return __ffma2_rn(a, b, c);
+}
+
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// one packed conversion (round to nearest even)
+__device__ __forceinline__ uint32_t pack2(const float2& x) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Columns 4 i .. 4 i + 3 of a staged row, bf16 (kBf16) or fp32, as two pairs.
+template <bool kBf16>
+__device__ __forceinline__ void staged22(const uint8_t* row, int i, float2 (&x)[2]) {
+  if constexpr (kBf16) {
+    const uint2 w = reinterpret_cast<const uint2*>(row)[i];
+    x[0] = unpack2(w.x);
+    x[1] = unpack2(w.y);
+  } else {
+    const float4 v = reinterpret_cast<const float4*>(row)[i];
+    x[0] = make_float2(v.x, v.y);
+    x[1] = make_float2(v.z, v.w);
+  }
+}
+
 // Columns 4 i .. 4 i + 3 of a staged row, bf16 (kBf16) or fp32.
 template <bool kBf16>
 __device__ __forceinline__ void staged4(const uint8_t* row, int i, float (&x)[4]) {
