@@ -403,12 +403,12 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const ColumnSum s0, con
   }
 }
 
-// Row lanes of the whole grid at most, over the shapes that a width can take: blocks of 4096 columns,
-// two per SM, or one of 8192.
+// Row lanes of the whole grid at most, over the shapes that a width can take.
 int max_units(int d, int sms) {
-  if (d <= 512) return 16 * sms;
-  if (d <= 1024) return 8 * sms;
-  if (d <= 2048) return 4 * sms;
+  if (d <= 256) return 16 * sms;
+  if (d <= 512) return 8 * sms;
+  if (d <= 1024) return 4 * sms;
+  if (d <= 2048) return 2 * sms;
   if (d <= 4096) return 2 * sms;
   return sms;
 }
@@ -555,9 +555,9 @@ cudaError_t launch_block_norm_bwd(const BlockNormBwdDev& p, cudaStream_t stream,
   const int d = p.d;
   int blocks = 0;
   if (d <= 256) e = run<32, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
-  else if (d <= 512) e = wide ? run<32, 4, 1>(a, g, yb, hf, blocks, stream, num_sms) : run<64, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
-  else if (d <= 1024) e = wide ? run<64, 4, 1>(a, g, yb, hf, blocks, stream, num_sms) : run<128, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
-  else if (d <= 2048) e = wide ? run<128, 4, 1>(a, g, yb, hf, blocks, stream, num_sms) : run<256, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
+  else if (d <= 512) e = run<64, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
+  else if (d <= 1024) e = run<128, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
+  else if (d <= 2048) e = run<256, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
   else if (d <= 4096) e = wide ? run<256, 4, 1>(a, g, yb, hf, blocks, stream, num_sms) : run<512, 2, 1>(a, g, yb, hf, blocks, stream, num_sms);
   else if (d <= 8192) e = wide ? run<512, 4, 1>(a, g, yb, hf, blocks, stream, num_sms) : run<512, 2, 2>(a, g, yb, hf, blocks, stream, num_sms);
   else e = wide ? run<512, 4, 2>(a, g, yb, hf, blocks, stream, num_sms) : run<512, 2, 4>(a, g, yb, hf, blocks, stream, num_sms);
