@@ -76,8 +76,27 @@ __device__ __forceinline__ float bn_rstd(double ss, double d, double eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(static_cast<float>(ss / d + eps)));
 }
 
+// int8 code of x in the low byte
+__device__ __forceinline__ uint32_t code(float x, float s) {
+  return __float_as_uint(__fadd_rn(__fmul_rn(x, s), kBnMagic));
+}
+
+// fp64 sum of the squares of a thread's columns, in four chains (one would wait for each addition).
+template <int VPT>
+__device__ __forceinline__ double sum_squares(const float2 (&x)[VPT][2]) {
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const double v[4] = {static_cast<double>(x[k][0].x), static_cast<double>(x[k][0].y),
+                         static_cast<double>(x[k][1].x), static_cast<double>(x[k][1].y)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = fma(v[j], v[j], s[j]);
+  }
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
 template <int TPR, int VPT, bool YB, bool HF>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const BlockNormArgs a) {
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR > 256 ? (VPT == 2 ? 2 : 1) : (VPT == 8 ? 2 : VPT == 4 ? 3 : 4)) block_norm_kernel(const BlockNormArgs a) {
   constexpr int THREADS = TPR < 256 ? 256 : TPR;
   constexpr int RPB = THREADS / TPR;
   __shared__ double s_y[THREADS / 32], s_h[THREADS / 32];
@@ -122,90 +141,80 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
     const int slot = pos.slot;
     if (active) mbar_wait(&bars[slot], pos.parity, &s_abort, a.err);
     pos.next(a.depth);
-    float y[VPT][4];
+    float2 y[VPT][2];
+    uint2 gain[VPT], gate[VPT];
+    // gains and gate row on their way before the sums that their use waits for
+    auto fetch = [&](const uint2* p, uint2 (&to)[VPT]) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int i = tr + k * TPR;
+        to[k] = i < a.nv ? __ldg(p + i) : make_uint2(0u, 0u);
+      }
+    };
+    if (a.gate != nullptr) fetch(a.gate + static_cast<long long>(rc / a.period) * a.nv, gate);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = tr + k * TPR;
-      if (active && i < a.nv) {
-        staged4<YB>(staged, i, y[k]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = 0.0f;
-      }
+      y[k][0] = y[k][1] = make_float2(0.0f, 0.0f);
+      if (active && i < a.nv) staged22<YB>(staged, i, y[k]);
     }
     float r1 = 1.0f;
     if (a.g_post != nullptr) {
-      double ss = 0.0;
-#pragma unroll
-      for (int k = 0; k < VPT; ++k)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const double v = static_cast<double>(y[k][j]);
-          ss = fma(v, v, ss);
-        }
+      fetch(a.g_post, gain);
+      double ss = sum_squares(y);
       ss = bn_reduce<TPR, THREADS, double>(ss, s_y, rib, false);
       r1 = bn_rstd(ss, d, eps);
+      const float2 r1v = splat2(r1);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int i = tr + k * TPR;
-        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (i < a.nv) unpack4(__ldg(a.g_post + i), g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(__fmul_rn(y[k][j], r1), g[j]);
+        y[k][0] = mul2(mul2(y[k][0], r1v), unpack2(gain[k].x));
+        y[k][1] = mul2(mul2(y[k][1], r1v), unpack2(gain[k].y));
       }
     }
     if (a.gate != nullptr) {
-      const uint2* gr = a.gate + static_cast<long long>(rc / a.period) * a.nv;
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int i = tr + k * TPR;
-        float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (i < a.nv) unpack4(__ldg(gr + i), g);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(g[j], y[k][j]);
+        y[k][0] = mul2(unpack2(gate[k].x), y[k][0]);
+        y[k][1] = mul2(unpack2(gate[k].y), y[k][1]);
       }
     }
-    double ss = 0.0;
+    fetch(a.g_pre, gain);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = tr + k * TPR;
       if (active && i < a.nv) {
-        float h[4];
-        staged4<!HF>(staged + y_bytes, i, h);
+        float2 h[2];
+        staged22<!HF>(staged + y_bytes, i, h);
+        // y is h' from here on
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = __fadd_rn(__fmul_rn(a.res_scale, h[j]), y[k][j]);
+        for (int j = 0; j < 2; ++j)
+          y[k][j] = make_float2(__fadd_rn(__fmul_rn(a.res_scale, h[j].x), y[k][j].x),
+                                __fadd_rn(__fmul_rn(a.res_scale, h[j].y), y[k][j].y));
         if constexpr (HF) {
-          static_cast<float4*>(a.H_out)[at + i] = make_float4(h[0], h[1], h[2], h[3]);
+          static_cast<float4*>(a.H_out)[at + i] = make_float4(y[k][0].x, y[k][0].y, y[k][1].x, y[k][1].y);
         } else {
-          const uint2 w = pack4(h);
+          const uint2 w = make_uint2(pack2(y[k][0]), pack2(y[k][1]));
           static_cast<uint2*>(a.H_out)[at + i] = w;
-          unpack4(w, h);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[k][j] = h[j];  // the row is h' from here on
-          const double v = static_cast<double>(h[j]);
-          ss = fma(v, v, ss);
+          y[k][0] = unpack2(w.x);
+          y[k][1] = unpack2(w.y);
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[k][j] = 0.0f;
+        y[k][0] = y[k][1] = make_float2(0.0f, 0.0f);
       }
     }
+    double ss = sum_squares(y);
     ss = bn_reduce<TPR, THREADS, double>(ss, s_h, rib, false);
     // every thread of the group has its columns in registers
     if (tr == 0 && row + a.depth * stride < a.T) request(row + a.depth * stride, slot);
     const float r2 = bn_rstd(ss, d, eps);
+    const float2 r2v = splat2(r2);
     uint32_t mx = 0u;
     uint2 xn[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int i = tr + k * TPR;
-      float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (i < a.nv) unpack4(__ldg(a.g_pre + i), g);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[k][j] = __fmul_rn(__fmul_rn(y[k][j], r2), g[j]);
-      xn[k] = pack4(y[k]);
+      xn[k] = make_uint2(pack2(mul2(mul2(y[k][0], r2v), unpack2(gain[k].x))),
+                         pack2(mul2(mul2(y[k][1], r2v), unpack2(gain[k].y))));
       if (i < a.nv) {
         mx = __vmaxu2(mx, __vmaxu2(xn[k].x & 0x7FFF7FFFu, xn[k].y & 0x7FFF7FFFu));
         if (active && a.Xn != nullptr) a.Xn[at + i] = xn[k];
@@ -231,12 +240,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) block_norm_kernel(const
       for (int k = 0; k < VPT; ++k) {
         const int i = tr + k * TPR;
         if (i >= a.nv) continue;
-        float x[4];
-        unpack4(xn[k], x);
-        uint32_t q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(__fadd_rn(__fmul_rn(x[j], sc), kBnMagic));
-        const uint32_t w = __byte_perm(__byte_perm(q[0], q[1], 0x0040u), __byte_perm(q[2], q[3], 0x0040u), 0x5410u);
+        const float2 x0 = unpack2(xn[k].x), x1 = unpack2(xn[k].y);
+        const uint32_t q0 = code(x0.x, sc), q1 = code(x0.y, sc), q2 = code(x1.x, sc), q3 = code(x1.y, sc);
+        const uint32_t w = __byte_perm(__byte_perm(q0, q1, 0x0040u), __byte_perm(q2, q3, 0x0040u), 0x5410u);
         a.Xq[at + i] = finite ? w : 0u;
       }
     }
@@ -271,7 +277,7 @@ cudaError_t dispatch(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
   if (a.T > 4 * num_sms) {
     // many rows: 32 columns per thread
     if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 4, stream, num_sms);
-    if (a.nv <= 32 * 4) return run<32, 4, YB, HF>(a, 4, stream, num_sms);
+    if (a.nv <= 32 * 4) return run<32, 4, YB, HF>(a, 3, stream, num_sms);
     if (a.nv <= 32 * 8) return run<32, 8, YB, HF>(a, 2, stream, num_sms);
     if (a.nv <= 64 * 8) return run<64, 8, YB, HF>(a, 2, stream, num_sms);
     if (a.nv <= 128 * 8) return run<128, 8, YB, HF>(a, 2, stream, num_sms);

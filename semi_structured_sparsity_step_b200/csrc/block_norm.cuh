@@ -11,21 +11,9 @@
 
 namespace sbl {
 
-__device__ __forceinline__ void unpack4(const uint2& w, float (&x)[4]) {
-  x[0] = __uint_as_float(w.x << 16);
-  x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(w.y << 16);
-  x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-}
-
-// one packed conversion (round to nearest even) per pair
-__device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(x[2], x[3]);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
-// Two fp32 operations per instruction (sm_100), each rounded as the single one.
+// Two fp32 operations per instruction (sm_100), each rounded as the single one.  The compiler fuses a
+// packed product with a packed sum, whatever rounding they name (measured: h' then differs in its
+// last bit), so a sum that has to see the rounded product is written with the single instructions.
 __device__ __forceinline__ float2 splat2(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float2 mul2(const float2& a, const float2& b) { return __fmul2_rn(a, b); }
 __device__ __forceinline__ float2 add2(const float2& a, const float2& b) { return __fadd2_rn(a, b); }
@@ -54,29 +42,6 @@ __device__ __forceinline__ void staged22(const uint8_t* row, int i, float2 (&x)[
     const float4 v = reinterpret_cast<const float4*>(row)[i];
     x[0] = make_float2(v.x, v.y);
     x[1] = make_float2(v.z, v.w);
-  }
-}
-
-// Columns 4 i .. 4 i + 3 of a staged row, bf16 (kBf16) or fp32.
-template <bool kBf16>
-__device__ __forceinline__ void staged4(const uint8_t* row, int i, float (&x)[4]) {
-  if constexpr (kBf16) {
-    unpack4(reinterpret_cast<const uint2*>(row)[i], x);
-  } else {
-    const float4 v = reinterpret_cast<const float4*>(row)[i];
-    x[0] = v.x;
-    x[1] = v.y;
-    x[2] = v.z;
-    x[3] = v.w;
-  }
-}
-
-template <bool kBf16>
-__device__ __forceinline__ void store4(void* p, long long i, const float (&x)[4]) {
-  if constexpr (kBf16) {
-    static_cast<uint2*>(p)[i] = pack4(x);
-  } else {
-    static_cast<float4*>(p)[i] = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
 

@@ -120,8 +120,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
     if constexpr (EPI == kEpiFwd) {
       v = a.atomic_i32 ? __int2float_rn(static_cast<int>(r[j]))
                        : __fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale);
-    } else if constexpr (epi_w8(EPI)) {
-      v = __fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale);
     } else if constexpr (EPI == kEpiDx) {
       v = __fmul_rn(scale, __uint_as_float(r[j]));
     } else {
@@ -141,14 +139,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
   }
   __syncwarp();
   const int cq = (lane & 7) * 4;
-  float4 sw = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // 8-bit product: the scales of this lane's four columns
-  if constexpr (epi_w8(EPI)) {
-    if (col0 + cq < a.N) {
-      const float4 w = __ldg(reinterpret_cast<const float4*>(a.wmax + col0 + cq));
-      sw = make_float4(__fdiv_rn(w.x, 127.0f), __fdiv_rn(w.y, 127.0f), __fdiv_rn(w.z, 127.0f),
-                       __fdiv_rn(w.w, 127.0f));
-    }
-  }
 #pragma unroll
   for (int it = 0; it < 8; ++it) {
     const int rr = it * 4 + (lane >> 3);
@@ -157,15 +147,6 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
     if (grow < a.M && gcol < a.N) {  // N % 8 == 0: a float4 is either all in or all out
       const float* t = tile + rr * 33 + cq;
       float4 v = make_float4(t[0], t[1], t[2], t[3]);
-      if constexpr (epi_w8(EPI))
-        v = make_float4(__fmul_rn(v.x, sw.x), __fmul_rn(v.y, sw.y), __fmul_rn(v.z, sw.z), __fmul_rn(v.w, sw.w));
-      if constexpr (EPI == kEpiW8Bf16) {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + static_cast<long long>(grow) * a.ldo +
-                                  gcol) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-        continue;
-      }
       float* dst = a.out + static_cast<long long>(grow) * a.ldo + gcol;
       if constexpr (EPI == kEpiFwd) {
         if (a.atomic_i32) {
@@ -190,6 +171,60 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
         }
       }
       *reinterpret_cast<float4*>(dst) = v;
+    }
+  }
+  __syncwarp();
+}
+
+// The same for the 8-bit product: scale (the token's) and sw (the chunk's 32 columns', in shared
+// memory) both in the row layout, so a bf16 chunk is packed before it is turned around and passes
+// shared memory at half the size, 16 bytes per lane and access.
+template <bool kBf16>
+__device__ __forceinline__ void epilogue_chunk_w8(const GemmArgs& a, float* tile, int row0, int col0, int lane,
+                                                  const uint32_t (&r)[32], float scale, const float* sw) {
+  if constexpr (kBf16) {
+    constexpr int LD = 20;  // words per row of 16 (32 columns): 16-byte accesses of 8 rows hit every bank once
+    uint32_t* t = reinterpret_cast<uint32_t*>(tile);
+#pragma unroll
+    for (int j = 0; j < 32; j += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 s = *reinterpret_cast<const float2*>(sw + j + 2 * k);
+        const __nv_bfloat162 p =
+            __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k])), scale), s.x),
+                                  __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k + 1])), scale), s.y));
+        w[k] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(t + lane * LD + j / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    const int cq = (lane & 3) * 8;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int rr = it * 8 + (lane >> 2);
+      if (row0 + rr < a.M && col0 + cq < a.N)  // N % 8 == 0
+        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                  static_cast<long long>(row0 + rr) * a.ldo + col0 + cq) =
+            *reinterpret_cast<const uint4*>(t + rr * LD + cq / 2);
+    }
+  } else {
+    constexpr int LD = 33;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const float2 s = *reinterpret_cast<const float2*>(sw + j);
+      tile[lane * LD + j] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale), s.x);
+      tile[lane * LD + j + 1] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 1])), scale), s.y);
+    }
+    __syncwarp();
+    const int cq = (lane & 7) * 4;
+#pragma unroll
+    for (int it = 0; it < 8; ++it) {
+      const int rr = it * 4 + (lane >> 3);
+      const float* t = tile + rr * LD + cq;
+      if (row0 + rr < a.M && col0 + cq < a.N)
+        *reinterpret_cast<float4*>(a.out + static_cast<long long>(row0 + rr) * a.ldo + col0 + cq) =
+            make_float4(t[0], t[1], t[2], t[3]);
     }
   }
   __syncwarp();
@@ -388,7 +423,8 @@ struct Cfg2 {
   static constexpr int EPI_BYTES = 4 * EPI_WARP_FLOATS * 4;
   // Packed B (KP > 0): per-lane replicated decode tables after the barriers.
   static constexpr int LUT_BYTES = KP > 0 ? 256 * 32 * 8 + 256 * 8 : 0;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256 + LUT_BYTES;
+  static constexpr int SCALE_BYTES = 2 * 256 * 4;  // 8-bit product: the column scales of two tiles
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256 + LUT_BYTES + SCALE_BYTES;
   static constexpr int THREADS = KP > 0 ? 448 : 192;  // packed: + 8 decoder warps
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static constexpr uint32_t IDESC = instr_desc(kI8, 256, BN, kAMN, kBMN);
@@ -508,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* sel_bytes = smem + STAGES * C::STAGE_BYTES + C::EPI_BYTES + 256;  // KP > 0: [256][32] uint2
   uint2* sel_one = reinterpret_cast<uint2*>(sel_bytes + 256 * 32 * 8);        // KP > 0: [256] uint2
+  float* col_scale = reinterpret_cast<float*>(sel_bytes + C::LUT_BYTES);       // 8-bit product: [2][256]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -725,6 +762,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
       grp.locate(w, pi, mb, nb, sp);
       const GemmArgs& A = grp.args[pi];
       const int b = t & 1;
+      if constexpr (epi_w8(EPI)) {
+        // the tile's column scales, by the four epilogue warps while its products run; two buffers,
+        // as a warp may still be in the tile before
+        for (int c = (warp - 2) * 32 + lane; c < C::BN; c += 128)
+          col_scale[b * C::BN + c] = nb * C::BN + c < A.N ? __fdiv_rn(__ldg(A.wmax + nb * C::BN + c), 127.0f) : 0.0f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
       if (!mbar_wait(&tfull[b], static_cast<uint32_t>(t >> 1) & 1u, abort_flag, args.err)) {
         give_up();
         break;
@@ -749,7 +793,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
         uint32_t r[32];
         tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(32 * c), r);
         tmem_ld_wait();
-        epilogue_chunk<EPI>(A, tile, row0, col0, lane, r, scale);
+        if constexpr (epi_w8(EPI))
+          epilogue_chunk_w8<EPI == kEpiW8Bf16>(A, tile, row0, col0, lane, r, scale, col_scale + b * C::BN + 32 * c);
+        else
+          epilogue_chunk<EPI>(A, tile, row0, col0, lane, r, scale);
       }
       tc_fence_before();
       __syncwarp();
