@@ -204,27 +204,29 @@ __device__ __forceinline__ void epilogue_chunk_w8(const GemmArgs& a, float* tile
     for (int it = 0; it < 4; ++it) {
       const int rr = it * 8 + (lane >> 2);
       if (row0 + rr < a.M && col0 + cq < a.N)  // N % 8 == 0
-        *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
-                                  static_cast<long long>(row0 + rr) * a.ldo + col0 + cq) =
-            *reinterpret_cast<const uint4*>(t + rr * LD + cq / 2);
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
+                                        static_cast<long long>(row0 + rr) * a.ldo + col0 + cq),
+               *reinterpret_cast<const uint4*>(t + rr * LD + cq / 2));
     }
   } else {
-    constexpr int LD = 33;
+    constexpr int LD = 36;  // 16-byte accesses of 8 rows hit every bank once
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const float2 s = *reinterpret_cast<const float2*>(sw + j);
-      tile[lane * LD + j] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale), s.x);
-      tile[lane * LD + j + 1] = __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 1])), scale), s.y);
+    for (int j = 0; j < 32; j += 4) {
+      const float4 s = *reinterpret_cast<const float4*>(sw + j);
+      *reinterpret_cast<float4*>(tile + lane * LD + j) =
+          make_float4(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j])), scale), s.x),
+                      __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 1])), scale), s.y),
+                      __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2])), scale), s.z),
+                      __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 3])), scale), s.w));
     }
     __syncwarp();
     const int cq = (lane & 7) * 4;
 #pragma unroll
     for (int it = 0; it < 8; ++it) {
       const int rr = it * 4 + (lane >> 3);
-      const float* t = tile + rr * LD + cq;
       if (row0 + rr < a.M && col0 + cq < a.N)
-        *reinterpret_cast<float4*>(a.out + static_cast<long long>(row0 + rr) * a.ldo + col0 + cq) =
-            make_float4(t[0], t[1], t[2], t[3]);
+        __stcs(reinterpret_cast<float4*>(a.out + static_cast<long long>(row0 + rr) * a.ldo + col0 + cq),
+               *reinterpret_cast<const float4*>(tile + rr * LD + cq));
     }
   }
   __syncwarp();
@@ -419,11 +421,11 @@ struct Cfg2 {
   static constexpr int A_BYTES = 128 * 128;      // this CTA's 128 A rows
   static constexpr int B_BYTES = 128 * 128;      // this CTA's 128 B rows
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int EPI_WARP_FLOATS = 32 * 33;
+  static constexpr int EPI_WARP_FLOATS = 32 * 36;  // rows of 33 words, or 36 (the 8-bit product)
   static constexpr int EPI_BYTES = 4 * EPI_WARP_FLOATS * 4;
   // Packed B (KP > 0): per-lane replicated decode tables after the barriers.
   static constexpr int LUT_BYTES = KP > 0 ? 256 * 32 * 8 + 256 * 8 : 0;
-  static constexpr int SCALE_BYTES = 2 * 256 * 4;  // 8-bit product: the column scales of two tiles
+  static constexpr int SCALE_BYTES = 2 * BN * 4;  // 8-bit product: the column scales of two tiles
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256 + LUT_BYTES + SCALE_BYTES;
   static constexpr int THREADS = KP > 0 ? 448 : 192;  // packed: + 8 decoder warps
   static constexpr uint32_t TMEM_COLS = 2 * BN;
@@ -544,7 +546,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* sel_bytes = smem + STAGES * C::STAGE_BYTES + C::EPI_BYTES + 256;  // KP > 0: [256][32] uint2
   uint2* sel_one = reinterpret_cast<uint2*>(sel_bytes + 256 * 32 * 8);        // KP > 0: [256] uint2
-  float* col_scale = reinterpret_cast<float*>(sel_bytes + C::LUT_BYTES);       // 8-bit product: [2][256]
+  float* col_scale = reinterpret_cast<float*>(sel_bytes + C::LUT_BYTES);       // 8-bit product: [2][BN]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -756,6 +758,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
   } else {
     const int q = warp & 3;
     float* tile = epi_tiles + q * C::EPI_WARP_FLOATS;
+    // 8-bit product: each of the 128 epilogue threads holds two column maxima of the tile to come
+    const int et = (warp - 2) * 32 + lane;
+    float wmax_next[2] = {0.0f, 0.0f};
+    auto fetch_wmax = [&](int w) {
+      if (w >= grp.total) return;
+      int pi, mb, nb, sp;
+      grp.locate(w, pi, mb, nb, sp);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int c = nb * C::BN + et + 128 * k;
+        wmax_next[k] = c < grp.args[pi].N ? __ldg(grp.args[pi].wmax + c) : 0.0f;
+      }
+    };
+    if constexpr (epi_w8(EPI)) fetch_wmax(pair_id);
     int t = 0;
     for (int w = pair_id; w < grp.total; w += n_pairs, ++t) {
       int pi, mb, nb, sp;
@@ -763,10 +779,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
       const GemmArgs& A = grp.args[pi];
       const int b = t & 1;
       if constexpr (epi_w8(EPI)) {
-        // the tile's column scales, by the four epilogue warps while its products run; two buffers,
-        // as a warp may still be in the tile before
-        for (int c = (warp - 2) * 32 + lane; c < C::BN; c += 128)
-          col_scale[b * C::BN + c] = nb * C::BN + c < A.N ? __fdiv_rn(__ldg(A.wmax + nb * C::BN + c), 127.0f) : 0.0f;
+        // this tile's column scales, requested a tile ago; two buffers, as a warp may still be in the
+        // tile before
+#pragma unroll
+        for (int k = 0; k < 2; ++k) col_scale[b * C::BN + et + 128 * k] = __fdiv_rn(wmax_next[k], 127.0f);
+        fetch_wmax(w + n_pairs);
         asm volatile("bar.sync 1, 128;" ::: "memory");
       }
       if (!mbar_wait(&tfull[b], static_cast<uint32_t>(t >> 1) & 1u, abort_flag, args.err)) {
