@@ -10,10 +10,11 @@
 // With few tokens the product is bound by reading Wq once.  The weight rows are the M = 128
 // operand and the tokens the N operand (16 .. 256), so a short batch wastes no weight bandwidth;
 // the K range of a 128-row tile is split over a cluster of blocks so that every SM streams
-// weights, each through its own TMA ring.  The blocks of a cluster then exchange their int32
-// partial tiles through distributed shared memory: block r adds up the token columns r, r + CS, ...
-// of all of them.  int32 sums are exact in any order.  A warp writes 32 neighbouring outputs of a
-// token.  Barriers, tensor memory and descriptors are set up while the previous kernel finishes
+// weights, each through its own TMA ring.  The blocks of a cluster then add their int32 partial
+// tiles up through distributed shared memory, each block a share of the token columns, by bulk
+// reductions into its shared memory (reading the other blocks' tiles word by word instead pays their
+// latency over and over: 28 us against 8 at 256 x 2048 x 2048 in four splits).  int32 sums are exact
+// in any order.  A warp writes 32 neighbouring outputs of a token.  Barriers, tensor memory and descriptors are set up while the previous kernel finishes
 // (programmatic dependent launch); global memory is touched only after it has.
 // Every mbarrier wait is bounded (sbl_device.cuh).
 #include <cuda.h>
@@ -47,14 +48,18 @@ struct W8Cfg {
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int PART_BYTES = BN * kW8Rows * 4;  // a block's partial tile, over the ring
   static constexpr int RING_BYTES = STAGES * STAGE_BYTES > PART_BYTES ? STAGES * STAGE_BYTES : PART_BYTES;
-  static constexpr int SMEM_BYTES = RING_BYTES + 1024 /*align*/ + BN * 4 + 256;
+  static constexpr int SX = BN < 32 ? 32 : BN;  // token scales (read 32 at a time)
+  static constexpr int SMEM_BYTES = RING_BYTES + 1024 /*align*/ + SX * 4 + 256;
   static constexpr uint32_t TMEM_COLS = BN < 32 ? 32 : BN;
   static constexpr uint32_t IDESC = instr_desc(true, kW8Rows, BN, false, false);
 };
 
+__device__ __forceinline__ float w8_scaled(int acc, float sx, float sw) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+}
+
 template <bool kBf16>
-__device__ __forceinline__ void w8_store(void* Y, long long at, int acc, float sx, float sw) {
-  const float y = __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+__device__ __forceinline__ void w8_store(void* Y, long long at, float y) {
   if constexpr (kBf16)
     static_cast<__nv_bfloat16*>(Y)[at] = __float2bfloat16_rn(y);
   else
@@ -69,10 +74,11 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* s_sx = reinterpret_cast<float*>(smem + C::RING_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + BN * 4);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + C::SX * 4);
   uint64_t* empty = full + STAGES;
   uint64_t* done = empty + STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  uint64_t* joined = done + 1;  // the other blocks' partial sums have arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5;
@@ -92,6 +98,7 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
+    mbar_init(joined, 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmW);
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
     const int row = 32 * q + lane;
     const int o = m0 + row;
     pdl::wait();
-    for (int c = threadIdx.x - 64; c < BN; c += 128)
+    for (int c = threadIdx.x - 64; c < C::SX; c += 128)
       s_sx[c] = n0 + c < a.T ? __fdiv_rn(a.amax[n0 + c], 127.0f) : 0.0f;
     const float sw = o < a.d_out ? __fdiv_rn(a.wmax[o], 127.0f) : 0.0f;
     asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -165,12 +172,22 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
       tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c0), r);
       tmem_ld_wait();
       if (cs == 1) {
-        if (o < a.d_out) {
+        // every result before the first store: a store could alias the scales for all the compiler
+        // knows, and each scale would wait for the store before it (65 cycles a column, measured)
+        float y[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j < cols)
-              w8_store<kBf16>(a.Y, static_cast<long long>(n0 + c0 + j) * a.d_out + o, static_cast<int>(r[j]),
-                              s_sx[c0 + j], sw);
+        for (int j = 0; j < 32; j += 4) {
+          const float4 sx = *reinterpret_cast<const float4*>(s_sx + c0 + j);
+          y[j] = w8_scaled(static_cast<int>(r[j]), sx.x, sw);
+          y[j + 1] = w8_scaled(static_cast<int>(r[j + 1]), sx.y, sw);
+          y[j + 2] = w8_scaled(static_cast<int>(r[j + 2]), sx.z, sw);
+          y[j + 3] = w8_scaled(static_cast<int>(r[j + 3]), sx.w, sw);
+        }
+        if (o < a.d_out) {
+          long long at = static_cast<long long>(n0 + c0) * a.d_out + o;
+#pragma unroll
+          for (int j = 0; j < 32; ++j, at += a.d_out)
+            if (c0 + j < cols) w8_store<kBf16>(a.Y, at, y[j]);
         }
       } else {
 #pragma unroll
@@ -180,43 +197,52 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
     }
   }
   if (cs > 1) {
+    // Block r ends up with the token columns [r share, (r + 1) share): every other block adds its
+    // partial sums of them into r's tile, one bulk reduction per pair of blocks.
+    const int cols = min(BN, a.T - n0);
+    const int share = (cols + static_cast<int>(cs) - 1) / static_cast<int>(cs);
+    auto first_of = [&](uint32_t r) { return min(cols, static_cast<int>(r) * share); };
+    const int c_lo = first_of(rank), c_hi = first_of(rank + 1);
+    if (threadIdx.x == 64) mbar_arrive_expect_tx(joined, static_cast<uint32_t>(c_hi - c_lo) * kW8Rows * 4u * (cs - 1));
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the tile was written by ordinary stores
     __syncwarp();
     pair::cluster_sync();  // every block's partial tile is in its shared memory
-    if (warp >= 2) {
+    if (threadIdx.x == 64) {
+      for (uint32_t d = 1; d < cs; ++d) {
+        const uint32_t p = rank + d < cs ? rank + d : rank + d - cs;
+        const int lo = first_of(p), n = first_of(p + 1) - lo;
+        if (n == 0) continue;
+        const uint32_t src = smem_u32(smem) + static_cast<uint32_t>(lo) * (kW8Rows * 4u);
+        asm volatile(
+            "cp.reduce.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes.add.s32 [%0], [%1], %2, [%3];" ::"r"(
+                pair::map_to(src, p)),
+            "r"(src), "r"(static_cast<uint32_t>(n) * kW8Rows * 4u), "r"(pair::map_to(smem_u32(joined), p))
+            : "memory");
+      }
+    }
+    if (warp >= 2 && c_hi > c_lo) {
+      mbar_wait(joined, 0, abort_flag, a.err);
       const int row = 32 * (warp & 3) + lane;
       const int o = m0 + row;
-      const int cols = min(BN, a.T - n0);
       const float sw = o < a.d_out ? __fdiv_rn(a.wmax[o], 127.0f) : 0.0f;
-      const uint32_t base = smem_u32(smem) + static_cast<uint32_t>(row) * 4u;
-      // eight columns at a time from every block: up to 64 remote loads in flight
-      for (int c0 = static_cast<int>(rank); c0 < cols; c0 += 8 * static_cast<int>(cs)) {
-        int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll
-        for (uint32_t p = 0; p < 8; ++p) {
-          if (p >= cs) break;
-          const uint32_t from = pair::map_to(base, p);
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int c = c0 + u * static_cast<int>(cs);
-            int v = 0;
-            if (c < cols)
-              asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                           : "=r"(v)
-                           : "r"(from + static_cast<uint32_t>(c) * (kW8Rows * 4u))
-                           : "memory");
-            acc[u] += v;
-          }
-        }
+      const int32_t* part = reinterpret_cast<const int32_t*>(smem) + row;
+      for (int c0 = c_lo; c0 < c_hi; c0 += 8) {
+        float y[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const int c = c0 + u * static_cast<int>(cs);
-          if (c < cols && o < a.d_out)
-            w8_store<kBf16>(a.Y, static_cast<long long>(n0 + c) * a.d_out + o, acc[u], s_sx[c], sw);
+          const int c = min(c0 + u, c_hi - 1);
+          y[u] = w8_scaled(part[c * kW8Rows], s_sx[c], sw);
+        }
+        if (o < a.d_out) {
+          long long at = static_cast<long long>(n0 + c0) * a.d_out + o;
+#pragma unroll
+          for (int u = 0; u < 8; ++u, at += a.d_out)
+            if (c0 + u < c_hi) w8_store<kBf16>(a.Y, at, y[u]);
         }
       }
     }
     __syncwarp();
-    pair::cluster_sync();  // no block leaves while its partial tile is being read
+    pair::cluster_sync();  // no block leaves while its tile is being added to or read
   }
   tc_fence_before();
   __syncthreads();
@@ -227,41 +253,86 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
 }
 
 template <int BN, int STAGES, bool kBf16>
-cudaError_t run(const int8_t* Xq, const int8_t* Wq, int d_in, W8Args a, int blocks_per_sm, cudaStream_t stream,
-                int num_sms) {
+cudaError_t run(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args& a, int cs, cudaStream_t stream) {
   using C = W8Cfg<BN, STAGES>;
   CUtensorMap tw, tx;
   if (!make_tmap_u8(&tw, Wq, d_in, a.d_out, d_in, 128, kW8Rows, true) ||
       !make_tmap_u8(&tx, Xq, d_in, a.T, d_in, 128, BN, true))
     return cudaErrorInvalidValue;
   auto kern = w8a8_stream_kernel<BN, STAGES, kBf16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int tiles = a.mt * ((a.T + BN - 1) / BN);
-  // as many K splits as keep the whole grid resident, at least two K blocks each
-  int cs = 8;
-  while (cs > 1 && (static_cast<long long>(tiles) * cs > static_cast<long long>(num_sms) * blocks_per_sm ||
-                    a.KB < 2 * cs))
-    --cs;
   return pdl::launch(kern, tiles * cs, kW8Threads, C::SMEM_BYTES, cs, stream, tw, tx, a);
 }
 
+// Which kernel a product goes to: token tile (0: the CTA-pair kernel) and K splits.
+struct W8Plan {
+  int bn, cs;
+};
+
+// The fastest by a model of the time in ns, fitted to 36 shapes (T 1 .. 8192, d_in 128 .. 11008, d_out
+// 128 .. 32768), on which the plan it picks is within 11% of the fastest of all token tiles and splits:
+//   streaming kernel: 3200 for the launch, plus the longer of
+//     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 180 bytes/ns, or 110
+//     with one ring of about 100 KB in flight, and
+//     Wq from HBM at 6500 bytes/ns or 50 per busy SM, a quarter more for each further token tile,
+//   plus the end of a block, once per wave: 600 + 24 per token column, or 1500 + 26 with a cluster's
+//   exchange (and then one wave at most);
+//   CTA-pair kernel: 6200, plus for each wave of 256 x 256 tiles the longer of 263 per K block and the
+//   3900 of a tile's epilogue.
+// Measured, best plan against one fixed choice (token tile >= T, as many splits as fit):
+// 512 x 2048 x 2048 7.6 us against 12.4, 256 x 2048 x 2048 7.5 against 19.9, 1 x 2048 x 32768 13.7
+// against 22.5 on CTA pairs, 2048 x 896 x 4864 17.0 on CTA pairs against 20.5.
+W8Plan plan_w8a8(int T, int d_in, int d_out, int num_sms) {
+  const double KB = (d_in + 127) / 128, mt = (d_out + kW8Rows - 1) / kW8Rows;
+  const double pair_tiles = static_cast<double>((T + 255) / 256) * ((d_out + 255) / 256);
+  const double pairs = num_sms / 2;
+  const double pair_wave = KB * 263.0 > 3900.0 ? KB * 263.0 : 3900.0;
+  double best = 6200.0 + static_cast<double>(static_cast<long long>((pair_tiles + pairs - 1) / pairs)) * pair_wave;
+  W8Plan plan{0, 1};
+  for (int bn = 16; bn <= 256; bn *= 2) {
+    const double nt = (T + bn - 1) / bn;
+    for (int cs = 1; cs <= 8 && (cs == 1 || 2 * cs <= KB); ++cs) {
+      const double blocks = mt * nt * cs;
+      const double per_sm = static_cast<double>(static_cast<long long>((blocks + num_sms - 1) / num_sms));
+      const double kb = static_cast<double>(static_cast<long long>((KB + cs - 1) / cs));
+      const double copy = per_sm * kb * (16384.0 + 128.0 * bn) / (per_sm > 1 || bn == 256 ? 180.0 : 110.0);
+      const double rate = blocks * 50.0 < 6500.0 ? blocks * 50.0 : 6500.0;
+      const double hbm = static_cast<double>(d_out) * d_in * (1.0 + 0.25 * (nt - 1)) / rate;
+      // clusters do not pack every SM: 264 of 296 places are counted on (288 were measured to take two waves)
+      const double resident = num_sms * (bn == 256 ? 1.0 : 2.0) * (cs == 1 ? 1.0 : bn == 256 ? 0.95 : 0.9);
+      const double waves = static_cast<double>(static_cast<long long>((blocks + resident - 1) / resident));
+      const double t =
+          3200.0 + (copy > hbm ? copy : hbm) + waves * (cs > 1 ? 1500.0 + 26.0 * bn : 600.0 + 24.0 * bn);
+      if ((cs == 1 || waves == 1) && t < best) {
+        best = t;
+        plan = W8Plan{bn, cs};
+      }
+    }
+    if (bn >= T) break;  // a wider tile only adds empty columns
+  }
+  return plan;
+}
+
 template <bool kBf16>
-cudaError_t dispatch(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args& a, cudaStream_t stream, int num_sms) {
-  if (a.T <= 16) return run<16, 6, kBf16>(Xq, Wq, d_in, a, 2, stream, num_sms);
-  if (a.T <= 32) return run<32, 5, kBf16>(Xq, Wq, d_in, a, 2, stream, num_sms);
-  if (a.T <= 64) return run<64, 4, kBf16>(Xq, Wq, d_in, a, 2, stream, num_sms);
-  if (a.T <= 128) return run<128, 3, kBf16>(Xq, Wq, d_in, a, 2, stream, num_sms);
-  return run<256, 4, kBf16>(Xq, Wq, d_in, a, 1, stream, num_sms);
+cudaError_t dispatch(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args& a, const W8Plan& p,
+                     cudaStream_t stream) {
+  switch (p.bn) {
+    case 16: return run<16, 6, kBf16>(Xq, Wq, d_in, a, p.cs, stream);
+    case 32: return run<32, 5, kBf16>(Xq, Wq, d_in, a, p.cs, stream);
+    case 64: return run<64, 4, kBf16>(Xq, Wq, d_in, a, p.cs, stream);
+    case 128: return run<128, 3, kBf16>(Xq, Wq, d_in, a, p.cs, stream);
+    default: return run<256, 4, kBf16>(Xq, Wq, d_in, a, p.cs, stream);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T, int d_in,
                         int d_out, bool y_bf16, void* Y, cudaStream_t stream, int num_sms, uint32_t* err) {
-  // The CTA-pair kernel wins once its 256 x 256 tiles fill the device.
-  const long long pair_tiles = static_cast<long long>((T + 255) / 256) * ((d_out + 255) / 256);
-  if (pair_tiles >= num_sms / 2)
+  const W8Plan p = plan_w8a8(T, d_in, d_out, num_sms);
+  if (p.bn == 0)
     return launch_forward_w8a8_pair(Xq, amax, Wq, wmax, T, d_in, d_out, y_bf16, Y, stream, num_sms, err);
   W8Args a{};
   a.amax = amax;
@@ -272,8 +343,7 @@ cudaError_t launch_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, c
   a.KB = (d_in + 127) / 128;
   a.mt = (d_out + kW8Rows - 1) / kW8Rows;
   a.err = err;
-  return y_bf16 ? dispatch<true>(Xq, Wq, d_in, a, stream, num_sms)
-                : dispatch<false>(Xq, Wq, d_in, a, stream, num_sms);
+  return y_bf16 ? dispatch<true>(Xq, Wq, d_in, a, p, stream) : dispatch<false>(Xq, Wq, d_in, a, p, stream);
 }
 
 }  // namespace sbl
