@@ -49,9 +49,9 @@ struct BlockNormArgs {
 
 template <int TPR, int THREADS, typename V>
 __device__ __forceinline__ V bn_reduce(V x, V* scratch, int rib, bool is_max) {
-  constexpr int WPR = TPR / 32;
+  constexpr int WPR = TPR < 32 ? 1 : TPR / 32;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     const V y = __shfl_xor_sync(0xFFFFFFFFu, x, o);
     x = is_max ? (x > y ? x : y) : x + y;
   }
@@ -272,24 +272,48 @@ cudaError_t run(BlockNormArgs a, int blocks_per_sm, cudaStream_t stream, int num
   return pdl::launch(kern, static_cast<int>(blocks), THREADS, smem, 1, stream, a);
 }
 
+// Threads per row and columns per thread.  Few rows want many threads per row (latency), many rows few
+// (what every thread does once per row, the sums and two square roots, is shared by more columns).
+// Measured, this choice against the other side of each rule, y fp32 and h bf16 unless said:
+//   32 threads (few rows: 2 vectors each) against 8 of 8: 256 columns, 16000 rows 14.0 us against 15.9,
+//     60000 rows 42.2 against 33.8;
+//   896 columns: 1 row 2.4 us with 256 threads, 2.6 with 128; 1000 rows 4.4 with 128, 5.9 with 4 vectors
+//     each; 16000 rows 31.5 with 32 of 8, 35.1 with 64 of 4;
+//   2048 columns: 300 rows 3.7 us with 256 threads, 4.5 with 64 of 8; 16000 rows 60.3 with 64 of 8,
+//     68.5 with 128 of 4; with an fp32 stream 79.3 against 72.5 (8 vectors leave the ring too shallow);
+//   4096 columns: 300 rows 4.7 us with 256 of 4, 5.6 with 128 of 8; 16000 rows 126 against 117;
+//   8192 columns: 300 rows 8.1 us with 256 of 8, 9.9 with 512 of 4; 1 row 4.2 against 4.0.
 template <bool YB, bool HF>
 cudaError_t dispatch(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
-  if (a.T > 4 * num_sms) {
-    // many rows: 32 columns per thread
-    if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 4, stream, num_sms);
-    if (a.nv <= 32 * 4) return run<32, 4, YB, HF>(a, 3, stream, num_sms);
-    if (a.nv <= 32 * 8) return run<32, 8, YB, HF>(a, 2, stream, num_sms);
-    if (a.nv <= 64 * 8) return run<64, 8, YB, HF>(a, 2, stream, num_sms);
-    if (a.nv <= 128 * 8) return run<128, 8, YB, HF>(a, 2, stream, num_sms);
-    if (a.nv <= 256 * 8) return run<256, 8, YB, HF>(a, 2, stream, num_sms);
-    return run<512, 8, YB, HF>(a, 1, stream, num_sms);
+  const bool many = a.T > 4 * num_sms;
+  if (a.nv <= 64) {
+    if (a.T > 160 * num_sms) return run<8, 8, YB, HF>(a, 2, stream, num_sms);
+    return run<32, 2, YB, HF>(a, 4, stream, num_sms);
   }
-  if (a.nv <= 32 * 2) return run<32, 2, YB, HF>(a, 4, stream, num_sms);
-  if (a.nv <= 64 * 2) return run<64, 2, YB, HF>(a, 4, stream, num_sms);
-  if (a.nv <= 128 * 2) return run<128, 2, YB, HF>(a, 4, stream, num_sms);
-  if (a.nv <= 256 * 2) return run<256, 2, YB, HF>(a, 4, stream, num_sms);
-  if (a.nv <= 512 * 2) return run<512, 2, YB, HF>(a, 2, stream, num_sms);
-  if (a.nv <= 512 * 4) return run<512, 4, YB, HF>(a, 1, stream, num_sms);
+  if (a.nv <= 128)
+    return many ? run<32, 4, YB, HF>(a, 3, stream, num_sms) : run<64, 2, YB, HF>(a, 4, stream, num_sms);
+  if (a.nv <= 256 && a.T > num_sms) {
+    if (!many) return run<128, 2, YB, HF>(a, 4, stream, num_sms);
+    if constexpr (HF)
+      return run<64, 4, YB, HF>(a, 3, stream, num_sms);
+    else
+      return run<32, 8, YB, HF>(a, 2, stream, num_sms);
+  }
+  if (a.nv <= 512) {
+    if (!many) return run<256, 2, YB, HF>(a, 4, stream, num_sms);
+    if constexpr (HF)
+      return run<128, 4, YB, HF>(a, 3, stream, num_sms);
+    else
+      return run<64, 8, YB, HF>(a, 2, stream, num_sms);
+  }
+  if (a.nv <= 1024) {
+    if constexpr (!HF) {
+      if (many) return run<128, 8, YB, HF>(a, 2, stream, num_sms);
+    }
+    return run<256, 4, YB, HF>(a, 3, stream, num_sms);
+  }
+  if (a.nv <= 2048)
+    return a.T > num_sms ? run<256, 8, YB, HF>(a, 2, stream, num_sms) : run<512, 4, YB, HF>(a, 1, stream, num_sms);
   return run<512, 8, YB, HF>(a, 1, stream, num_sms);
 }
 

@@ -66,12 +66,12 @@ struct RingPos {
   }
 };
 
-// Barrier of the TPR threads of row lane `rib` (a warp of its own, or one named barrier per lane), so
+// Barrier of the TPR threads of row lane `rib` (within a warp, or one named barrier per lane), so
 // the lanes of a block keep their own pace.  A slot may be refilled behind it: every value read from
 // the slot has gone into the sums that the threads bring to the barrier.
 template <int TPR, int THREADS>
 __device__ __forceinline__ void lane_sync(int rib) {
-  if constexpr (TPR == 32)
+  if constexpr (TPR <= 32)
     __syncwarp();
   else if constexpr (TPR == THREADS)
     __syncthreads();

@@ -161,7 +161,7 @@ def test_types_and_parts(lib, y_bf16, h_f32, post, period):
 
 @pytest.mark.parametrize("T,d,period,readers", [(6000, 256, 250, 3), (4100, 896, 1000, 2), (1999, 2048, 667, 3),
                                                 (700, 4112, None, 1), (333, 8192, 5, 2), (5000, 64, 2, 1),
-                                                (3001, 512, 1, 1)])
+                                                (3001, 512, 1, 1), (24000, 256, 4096, 1), (23999, 48, 7, 2)])
 def test_batches_that_cut_groups_into_segments(lib, T, d, period, readers):
     """More tokens than row lanes: several rows and segments per lane, ragged last group."""
     c = Case(T, d, period=period, readers=readers, seed=T)
