@@ -10,9 +10,10 @@
 // and writes them once, where the floor is one read and one write.  Two launches: the first
 // leaves one fp64 partial sum per block, the second sums the partials (every block, in the
 // same order, so no block waits for another) and scales.  The scaling pass walks the tiles
-// backwards, so it starts with what the norm pass read last and L2 (126 MB) still holds;
-// gradients that fit there are read from HBM once.  No atomics: S is the same bits for the
-// same tensors on every run on one device.
+// backwards, so it starts with what the norm pass read last and asked L2 to hold; gradients that fit
+// there are read from HBM once.  No atomics: S is the same bits for the same tensors on every run on
+// one device.  Measured: norm pass alone 176 us for 1233 MB (7.0 TB/s), with clipping 586 us, where
+// reading all but 64 MB twice and writing once takes 555 us at the measured copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -26,6 +27,9 @@ namespace {
 constexpr int kGgThreads = 256;
 constexpr int kGgVecs = 4;                            // 16-byte vectors per thread and tile
 constexpr int kGgTileVecs = kGgThreads * kGgVecs;     // 16 KB per tile
+// The scaling pass is asked to find this much of the norm pass's last reads in L2.  Measured on
+// gradients of 1233 MB: 586 us with 48 to 96 MB, 591 with none, 596 with plain loads.
+constexpr unsigned kGgKeepTiles = (64u << 20) / (kGgTileVecs * 16);
 constexpr int kGgTensors = 128;                       // tensors per launch (the table is a kernel parameter)
 
 struct GradTable {
@@ -35,10 +39,35 @@ struct GradTable {
   unsigned int tile_start[kGgTensors + 1];
   unsigned int bf16[kGgTensors / 32];  // bit set: the tensor holds bf16
   int count;
+  int in_place;  // every out is its g
 };
 
 __device__ __forceinline__ void gg_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void gg_pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// L2 eviction priorities: `last` for what the scaling pass reads first, `first` for the rest.
+__device__ __forceinline__ uint64_t policy_last() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_first() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t pol) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p), "l"(pol));
+  return v;
+}
+__device__ __forceinline__ void store_hint(uint4* p, const uint4& v, uint64_t pol) {
+  asm volatile("st.global.L1::no_allocate.L2::cache_hint.v4.u32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "l"(pol)
+               : "memory");
+}
 
 __device__ __forceinline__ double sq_add(float x, double s) {
   const double d = static_cast<double>(x);
@@ -69,7 +98,7 @@ struct TileCursor {
 };
 
 template <bool kBf16>
-__device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n, unsigned long long v0, double s) {
+__device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n, unsigned long long v0, double s, uint64_t pol) {
   constexpr int PER = kBf16 ? 8 : 4;  // elements per vector
   const unsigned long long nv = n / PER;
   const uint4* gv = static_cast<const uint4*>(g);
@@ -77,7 +106,7 @@ __device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n
 #pragma unroll
   for (int k = 0; k < kGgVecs; ++k) {
     const unsigned long long i = v0 + k * kGgThreads + threadIdx.x;
-    v[k] = i < nv ? __ldg(gv + i) : make_uint4(0u, 0u, 0u, 0u);
+    v[k] = i < nv ? load_hint(gv + i, pol) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int k = 0; k < kGgVecs; ++k) {
@@ -106,19 +135,22 @@ __device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n
   return s;
 }
 
+// keep: tiles at the end of the table that L2 should hold until the scaling pass.
 __global__ void __launch_bounds__(kGgThreads) grad_sumsq_kernel(const __grid_constant__ GradTable tab,
-                                                                double* __restrict__ partial) {
+                                                                double* __restrict__ partial, unsigned keep) {
   __shared__ double scratch[kGgThreads / 32];
   gg_pdl_wait();
   gg_pdl_trigger();
   const unsigned total = tab.tile_start[tab.count];
+  const uint64_t last = policy_last(), first = policy_first();
   double s = 0.0;
   TileCursor c{0};
   for (unsigned t = blockIdx.x; t < total; t += gridDim.x) {
     c.seek(tab, t);
     const unsigned long long v0 = static_cast<unsigned long long>(t - tab.tile_start[c.p]) * kGgTileVecs;
-    s = ((tab.bf16[c.p >> 5] >> (c.p & 31)) & 1u) ? tile_sumsq<true>(tab.g[c.p], tab.n[c.p], v0, s)
-                                                  : tile_sumsq<false>(tab.g[c.p], tab.n[c.p], v0, s);
+    const uint64_t pol = total - t <= keep ? last : first;
+    s = ((tab.bf16[c.p >> 5] >> (c.p & 31)) & 1u) ? tile_sumsq<true>(tab.g[c.p], tab.n[c.p], v0, s, pol)
+                                                  : tile_sumsq<false>(tab.g[c.p], tab.n[c.p], v0, s, pol);
   }
   s = block_sum(s, scratch);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
@@ -155,6 +187,7 @@ __global__ void __launch_bounds__(kGgThreads) grad_norm_finish_kernel(const doub
 template <bool kBf16>
 __device__ __forceinline__ void tile_scale(const void* g, void* out, unsigned long long n, unsigned long long v0,
                                            float c) {
+  const uint64_t first = policy_first();
   constexpr int PER = kBf16 ? 8 : 4;
   const unsigned long long nv = n / PER;
   const uint4* gv = static_cast<const uint4*>(g);
@@ -163,7 +196,7 @@ __device__ __forceinline__ void tile_scale(const void* g, void* out, unsigned lo
 #pragma unroll
   for (int k = 0; k < kGgVecs; ++k) {
     const unsigned long long i = v0 + k * kGgThreads + threadIdx.x;
-    v[k] = i < nv ? __ldcs(gv + i) : make_uint4(0u, 0u, 0u, 0u);
+    v[k] = i < nv ? load_hint(gv + i, first) : make_uint4(0u, 0u, 0u, 0u);
   }
 #pragma unroll
   for (int k = 0; k < kGgVecs; ++k) {
@@ -179,7 +212,7 @@ __device__ __forceinline__ void tile_scale(const void* g, void* out, unsigned lo
         w[j] = __float_as_uint(__fmul_rn(__uint_as_float(w[j]), c));
       }
     }
-    if (i < nv) __stcs(ov + i, make_uint4(w[0], w[1], w[2], w[3]));
+    if (i < nv) store_hint(ov + i, make_uint4(w[0], w[1], w[2], w[3]), first);
   }
   if (v0 <= nv && nv < v0 + kGgTileVecs) {
     const unsigned long long e = nv * PER + threadIdx.x;
@@ -203,13 +236,13 @@ __global__ void __launch_bounds__(kGgThreads)
   const float c = clip_factor(S, max_norm);
   if (sumsq != nullptr) store_norm(S, c, sumsq, norm, clip);
   const unsigned total = tab.tile_start[tab.count];
-  if (blockIdx.x >= total) return;
+  if (blockIdx.x >= total || (c == 1.0f && tab.in_place != 0)) return;  // in place, below the limit: nothing to do
   TileCursor cur{tab.count - 1};
   for (unsigned u = blockIdx.x; u < total; u += gridDim.x) {
     const unsigned t = total - 1 - u;
     cur.seek_back(tab, t);
     const int p = cur.p;
-    if (c == 1.0f && tab.out[p] == tab.g[p]) continue;  // in place and below the limit: already the result
+    if (c == 1.0f && tab.out[p] == tab.g[p]) continue;
     const unsigned long long v0 = static_cast<unsigned long long>(t - tab.tile_start[p]) * kGgTileVecs;
     if ((tab.bf16[p >> 5] >> (p & 31)) & 1u)
       tile_scale<true>(tab.g[p], tab.out[p], tab.n[p], v0, c);
@@ -228,6 +261,7 @@ int gg_blocks(int num_sms) {
 // Fills the table with up to kGgTensors tensors from `i`; returns the index behind the last.
 int fill_table(const GradTensorDev* t, int i, int count, GradTable& tab) {
   tab.count = 0;
+  tab.in_place = 1;
   tab.tile_start[0] = 0;
   for (int k = 0; k < kGgTensors / 32; ++k) tab.bf16[k] = 0u;
   unsigned long long tiles = 0;
@@ -239,6 +273,7 @@ int fill_table(const GradTensorDev* t, int i, int count, GradTable& tab) {
     const int p = tab.count++;
     tab.g[p] = t[i].g;
     tab.out[p] = t[i].out;
+    if (t[i].out != t[i].g) tab.in_place = 0;
     tab.n[p] = t[i].n;
     if (t[i].bf16) tab.bf16[p >> 5] |= 1u << (p & 31);
     tiles += mine;
@@ -280,7 +315,8 @@ cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them,
     if (tab.count == 0) break;
     const unsigned total = tab.tile_start[tab.count];
     const int grid = static_cast<int>(total < static_cast<unsigned>(gg_blocks(num_sms)) ? total : gg_blocks(num_sms));
-    const cudaError_t e = gg_launch(grad_sumsq_kernel, grid, stream, tab, partial + used);
+    const cudaError_t e = gg_launch(grad_sumsq_kernel, grid, stream, tab, partial + used,
+                                    clip_them ? kGgKeepTiles : 0u);
     if (e != cudaSuccess) return e;
     used += grid;
   }
