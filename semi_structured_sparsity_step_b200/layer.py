@@ -7,6 +7,11 @@ operator runs in libsbl's kernels:
                       + sbl_compress24 for a 2:4 layer built with sparse24=True
     forward(X)     -> sbl_act_quant, sbl_forward (or sbl_forward_sparse24)
     backward(dY)   -> sbl_backward     (dX and the dense dW)
+
+and of what stands around it: the seam between two products (BlockNorm:
+sbl_block_norm and its backward), a projection in 8 bits (Int8Linear:
+sbl_forward_w8a8) and the clipped gradients of a step (GradClip:
+sbl_grad_clip_group).
 """
 from __future__ import annotations
 
@@ -59,3 +64,83 @@ class SparseBitLinearLayer:
 def act_quant(X: torch.Tensor, Xq: torch.Tensor, amax: torch.Tensor, stream=None):
     T, d_in = X.shape
     B.sbl_act_quant(X, T, d_in, Xq, amax, stream)
+
+
+class BlockNorm:
+    """Norm of a branch output, gate, scaled residual, next norm and int8 codes
+    (sbl_block_norm), with its backward, for up to `max_tokens` tokens.
+
+    g_pre, g_post: bf16 gains of the norms after and before the sum (g_post
+    None: the branch is not normalised).  The outputs and the factors that the
+    backward needs live here and are overwritten by the next call."""
+
+    def __init__(self, g_pre: torch.Tensor, g_post: torch.Tensor | None = None, max_tokens: int = 1,
+                 res_scale: float = 1.0, eps: float = 1e-6, y_dtype=torch.float32, h_dtype=torch.bfloat16):
+        assert g_pre.is_cuda and g_pre.dtype == torch.bfloat16
+        assert y_dtype in (torch.float32, torch.bfloat16) and h_dtype in (torch.float32, torch.bfloat16)
+        dev, d = g_pre.device, g_pre.numel()
+        self.g_pre, self.g_post, self.d, self.res_scale, self.eps = g_pre, g_post, d, res_scale, eps
+        self.flags = (B.SBL_BLOCK_Y_BF16 if y_dtype == torch.bfloat16 else 0) | \
+            (B.SBL_BLOCK_H_F32 if h_dtype == torch.float32 else 0)
+        self.H_out = torch.empty(max_tokens, d, dtype=h_dtype, device=dev)
+        self.Xn = torch.empty(max_tokens, d, dtype=torch.bfloat16, device=dev)
+        self.Xq = torch.empty(max_tokens, d, dtype=torch.int8, device=dev)
+        self.amax = torch.empty(max_tokens, dtype=torch.float32, device=dev)
+        self.rstd = torch.empty(2 * max_tokens, dtype=torch.float32, device=dev)
+        self.dg_pre = torch.zeros(d, dtype=torch.float32, device=dev)
+        self.dg_post = torch.zeros(d, dtype=torch.float32, device=dev) if g_post is not None else None
+        self.ws_bytes = B.sbl_block_norm_backward_workspace_bytes(d)
+        self.ws = None  # allocated by the first backward
+
+    def forward(self, Y, H, gate=None, gate_period=0, stream=None):
+        """-> (H_out, Xn, Xq, amax) of the call's tokens."""
+        T = Y.shape[0]
+        B.sbl_block_norm(Y, H, self.g_post, gate, gate_period, self.res_scale, self.g_pre, self.eps, T, self.d,
+                         self.flags, self.H_out, self.Xn, self.Xq, self.amax, self.rstd, stream)
+        return self.H_out[:T], self.Xn[:T], self.Xq[:T], self.amax[:T]
+
+    def backward(self, dXn, dH_out, Y, dY, dH, gate=None, gate_period=0, dgate=None, accumulate=False, stream=None):
+        """dXn: the gradients of Xn from each product that read it (1 to 3); the gains' gradients go
+        to dg_pre and dg_post.  Uses H_out and the factors of the last forward."""
+        if self.ws is None:
+            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
+        B.sbl_block_norm_backward(dXn, dH_out, Y, self.H_out, self.g_post, gate, gate_period, self.res_scale,
+                                  self.g_pre, self.rstd, Y.shape[0], self.d, self.flags, dY, dH, self.dg_post,
+                                  self.dg_pre, dgate, int(accumulate), self.ws, self.ws_bytes, stream)
+
+
+class Int8Linear:
+    """A projection held in 8 bits: W [d_out, d_in] bf16, quantised row by row once."""
+
+    def __init__(self, W: torch.Tensor):
+        assert W.is_cuda and W.dtype == torch.bfloat16 and W.is_contiguous()
+        self.d_out, self.d_in = W.shape
+        self.Wq = torch.empty(self.d_out, self.d_in, dtype=torch.int8, device=W.device)
+        self.wmax = torch.empty(self.d_out, dtype=torch.float32, device=W.device)
+        B.sbl_act_quant(W, self.d_out, self.d_in, self.Wq, self.wmax)
+
+    def forward(self, Xq, amax, Y, stream=None):
+        """Y [T, d_out] in fp32 or bf16, by its type."""
+        flags = B.SBL_W8A8_Y_BF16 if Y.dtype == torch.bfloat16 else 0
+        B.sbl_forward_w8a8(Xq, amax, self.Wq, self.wmax, Xq.shape[0], self.d_in, self.d_out, flags, Y, stream)
+
+
+class GradClip:
+    """The global norm of a step's gradients and the clip by it, over a fixed list of
+    tensors (fp32 or bf16), in place.  sumsq is what sbl_adamw_step takes as grad_sqnorm."""
+
+    def __init__(self, grads):
+        self.tensors = [(g, g, g.numel(), g.dtype == torch.bfloat16) for g in grads]
+        dev = grads[0].device
+        self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.factor = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.ws_bytes = B.sbl_grad_group_workspace_bytes(len(grads))
+        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+
+    def norm_only(self, stream=None):
+        B.sbl_grad_norm_group(self.tensors, self.sumsq, self.norm, self.ws, self.ws_bytes, stream)
+
+    def clip(self, max_norm: float, stream=None):
+        B.sbl_grad_clip_group(self.tensors, max_norm, self.sumsq, self.norm, self.factor, self.ws, self.ws_bytes,
+                              stream)
