@@ -8,6 +8,7 @@ is no fallback path.  Output tensors are allocated by the caller.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -218,22 +219,34 @@ def sbl_grad_group_workspace_bytes(count: int) -> int:
 
 
 def _grad_tensors(fn, tensors):
-    """tensors: sequence of (g, out_or_None, n, bf16) -> (checker, descriptor array, count)."""
+    """tensors: sequence of (g, out_or_None, n, bf16) -> (checker, descriptor array, count).
+
+    The checker's tests are written out in the loop: a step has hundreds of
+    gradients, and a call for each would cost more than the launches."""
     import torch
     a = _args(fn)
-    words = []
+    dev, f32, b16 = torch.cuda.current_device(), torch.float32, torch.bfloat16
+    words = array.array("Q")
     for g, out, n, bf16 in tensors:
-        dt = torch.bfloat16 if bf16 else torch.float32
+        dt = b16 if bf16 else f32
+        ptrs = []
+        for x in ((g,) if out is None or out is g else (g, out)):
+            if x.__class__ is int:
+                ptrs.append(x)
+            elif x.dtype is dt and x.numel() >= n and x.get_device() == dev and x.is_contiguous():
+                ptrs.append(x.data_ptr())
+            else:
+                raise SblError(fn, 1)
         # bf16 and the reserved word share the descriptor's last 8 bytes (little-endian)
-        words += (a(g, dt, n) or 0, a(out, dt, n) or 0, n, 1 if bf16 else 0)
-    return a, (ctypes.c_uint64 * max(1, len(words)))(*words), len(words) // 4
+        words.extend((ptrs[0], 0 if out is None else ptrs[-1], n, 1 if bf16 else 0))
+    return a, words, len(words) // 4
 
 
 def sbl_grad_norm_group(tensors, sumsq, norm, workspace, workspace_bytes, stream=None) -> None:
     """tensors: sequence of (g, None, n, bf16)."""
     import torch
     a, arr, count = _grad_tensors("sbl_grad_norm_group", tensors)
-    _call("sbl_grad_norm_group", ctypes.addressof(arr), count, a(sumsq, torch.float64, 1), a(norm, torch.float32, 1),
+    _call("sbl_grad_norm_group", arr.buffer_info()[0], count, a(sumsq, torch.float64, 1), a(norm, torch.float32, 1),
           a(workspace, torch.uint8, workspace_bytes), workspace_bytes, _stream(stream))
 
 
@@ -241,7 +254,7 @@ def sbl_grad_clip_group(tensors, max_norm, sumsq, norm, clip, workspace, workspa
     """tensors: sequence of (g, out, n, bf16); out may be g."""
     import torch
     a, arr, count = _grad_tensors("sbl_grad_clip_group", tensors)
-    _call("sbl_grad_clip_group", ctypes.addressof(arr), count, max_norm, a(sumsq, torch.float64, 1),
+    _call("sbl_grad_clip_group", arr.buffer_info()[0], count, max_norm, a(sumsq, torch.float64, 1),
           a(norm, torch.float32, 1), a(clip, torch.float32, 1), a(workspace, torch.uint8, workspace_bytes),
           workspace_bytes, _stream(stream))
 
