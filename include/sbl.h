@@ -349,7 +349,8 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
  *   dH_out     optional (NULL: zero): [T, d], type of H: the gradient of h'
  *              from its other readers.
  *   H_out, rstd, Y, g_post, gate, gate_period, res_scale, g_pre, flags: as
- *              in the forward call.
+ *              in the forward call.  Y is not read, and may be NULL, when
+ *              neither g_post nor dgate is given.
  *   dY         [T, d] bf16 out (the dY of the branch's product).
  *   dH         optional (NULL): [T, d] out, type of H; may be dH_out itself.
  *   dg_post, dg_pre [d], dgate [rows of gate, d]: optional (NULL), float out;

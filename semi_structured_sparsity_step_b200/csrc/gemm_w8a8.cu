@@ -37,7 +37,7 @@ struct W8Args {
   const float* wmax;
   void* Y;
   int T, d_out, KB;  // KB: 128-byte blocks of K
-  int mt;            // weight row tiles
+  int nt;            // token tiles
   uint32_t* err;
 };
 
@@ -87,8 +87,10 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(cs));
   rank = pair::cluster_rank();
   const int tile = static_cast<int>(blockIdx.x / cs);
-  const int m0 = (tile % a.mt) * kW8Rows;
-  const int n0 = (tile / a.mt) * BN;
+  // token tiles vary fastest: the blocks that read the same weight rows run together, and Wq comes from
+  // HBM once
+  const int m0 = (tile / a.nt) * kW8Rows;
+  const int n0 = (tile % a.nt) * BN;
   const int kb0 = static_cast<int>(static_cast<long long>(a.KB) * rank / cs);
   const int kb1 = static_cast<int>(static_cast<long long>(a.KB) * (rank + 1) / cs);
 
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
 }
 
 template <int BN, int STAGES, bool kBf16>
-cudaError_t run(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args& a, int cs, cudaStream_t stream) {
+cudaError_t run(const int8_t* Xq, const int8_t* Wq, int d_in, W8Args a, int cs, cudaStream_t stream) {
   using C = W8Cfg<BN, STAGES>;
   CUtensorMap tw, tx;
   if (!make_tmap_u8(&tw, Wq, d_in, a.d_out, d_in, 128, kW8Rows, true) ||
@@ -263,7 +265,8 @@ cudaError_t run(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args& a, i
   auto kern = w8a8_stream_kernel<BN, STAGES, kBf16>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int tiles = a.mt * ((a.T + BN - 1) / BN);
+  a.nt = (a.T + BN - 1) / BN;
+  const int tiles = (a.d_out + kW8Rows - 1) / kW8Rows * a.nt;
   return pdl::launch(kern, tiles * cs, kW8Threads, C::SMEM_BYTES, cs, stream, tw, tx, a);
 }
 
@@ -272,16 +275,18 @@ struct W8Plan {
   int bn, cs;
 };
 
-// The fastest by a model of the time in ns, fitted to 36 shapes (T 1 .. 8192, d_in 128 .. 11008, d_out
-// 128 .. 32768), on which the plan it picks is within 11% of the fastest of all token tiles and splits:
+// The fastest by a model of the time in ns, fitted to 43 shapes (T 1 .. 8192, d_in 128 .. 11008, d_out
+// 128 .. 32768), on which the plan it picks is within 6% of the fastest of all token tiles and splits
+// but for three (10, 13 and 16%):
 //   streaming kernel: 3200 for the launch, plus the longer of
-//     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 180 bytes/ns, or 110
+//     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 160 bytes/ns, or 110
 //     with one ring of about 100 KB in flight, and
-//     Wq from HBM at 6500 bytes/ns or 50 per busy SM, a quarter more for each further token tile,
+//     Wq from HBM at 6500 bytes/ns or 50 per block of the last wave, a quarter more for each further
+//     token tile,
 //   plus the end of a block, once per wave: 600 + 24 per token column, or 1500 + 26 with a cluster's
 //   exchange (and then one wave at most);
-//   CTA-pair kernel: 6200, plus for each wave of 256 x 256 tiles the longer of 263 per K block and the
-//   3900 of a tile's epilogue.
+//   CTA-pair kernel: 6200, plus the longer of both operands from HBM at 4500 bytes/ns and, for each wave
+//   of 256 x 256 tiles, the longer of 263 per K block and the 3900 of a tile's epilogue.
 // Measured, best plan against one fixed choice (token tile >= T, as many splits as fit):
 // 512 x 2048 x 2048 7.6 us against 12.4, 256 x 2048 x 2048 7.5 against 19.9, 1 x 2048 x 32768 13.7
 // against 22.5 on CTA pairs, 2048 x 896 x 4864 17.0 on CTA pairs against 20.5.
@@ -290,7 +295,9 @@ W8Plan plan_w8a8(int T, int d_in, int d_out, int num_sms) {
   const double pair_tiles = static_cast<double>((T + 255) / 256) * ((d_out + 255) / 256);
   const double pairs = num_sms / 2;
   const double pair_wave = KB * 263.0 > 3900.0 ? KB * 263.0 : 3900.0;
-  double best = 6200.0 + static_cast<double>(static_cast<long long>((pair_tiles + pairs - 1) / pairs)) * pair_wave;
+  const double pair_math = static_cast<double>(static_cast<long long>((pair_tiles + pairs - 1) / pairs)) * pair_wave;
+  const double pair_hbm = (static_cast<double>(d_out) + T) * d_in / 4500.0;
+  double best = 6200.0 + (pair_math > pair_hbm ? pair_math : pair_hbm);
   W8Plan plan{0, 1};
   for (int bn = 16; bn <= 256; bn *= 2) {
     const double nt = (T + bn - 1) / bn;
@@ -298,12 +305,14 @@ W8Plan plan_w8a8(int T, int d_in, int d_out, int num_sms) {
       const double blocks = mt * nt * cs;
       const double per_sm = static_cast<double>(static_cast<long long>((blocks + num_sms - 1) / num_sms));
       const double kb = static_cast<double>(static_cast<long long>((KB + cs - 1) / cs));
-      const double copy = per_sm * kb * (16384.0 + 128.0 * bn) / (per_sm > 1 || bn == 256 ? 180.0 : 110.0);
-      const double rate = blocks * 50.0 < 6500.0 ? blocks * 50.0 : 6500.0;
-      const double hbm = static_cast<double>(d_out) * d_in * (1.0 + 0.25 * (nt - 1)) / rate;
+      const double copy = per_sm * kb * (16384.0 + 128.0 * bn) / (per_sm > 1 || bn == 256 ? 160.0 : 110.0);
       // clusters do not pack every SM: 264 of 296 places are counted on (288 were measured to take two waves)
       const double resident = num_sms * (bn == 256 ? 1.0 : 2.0) * (cs == 1 ? 1.0 : bn == 256 ? 0.95 : 0.9);
       const double waves = static_cast<double>(static_cast<long long>((blocks + resident - 1) / resident));
+      const double last = (blocks - (waves - 1) * resident) / blocks;  // the last wave's share of the blocks
+      const double wq = static_cast<double>(d_out) * d_in * (1.0 + 0.25 * (nt - 1));
+      const double last_rate = last * blocks * 50.0 < 6500.0 ? last * blocks * 50.0 : 6500.0;
+      const double hbm = wq * (1.0 - last) / 6500.0 + wq * last / last_rate;
       const double t =
           3200.0 + (copy > hbm ? copy : hbm) + waves * (cs > 1 ? 1500.0 + 26.0 * bn : 600.0 + 24.0 * bn);
       if ((cs == 1 || waves == 1) && t < best) {
@@ -342,7 +351,6 @@ cudaError_t launch_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, c
   a.T = T;
   a.d_out = d_out;
   a.KB = (d_in + 127) / 128;
-  a.mt = (d_out + kW8Rows - 1) / kW8Rows;
   a.err = err;
   return y_bf16 ? dispatch<true>(Xq, Wq, d_in, a, p, stream) : dispatch<false>(Xq, Wq, d_in, a, p, stream);
 }

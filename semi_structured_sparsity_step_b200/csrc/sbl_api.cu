@@ -364,7 +364,8 @@ sbl_status sbl_block_norm_backward(const float* const* dXn, int readers, const v
     return SBL_ERR_INVALID_ARG;
   if ((dg_post != nullptr && g_post == nullptr) || (dgate != nullptr && gate == nullptr)) return SBL_ERR_INVALID_ARG;
   if (T > 0) {
-    if (Y == nullptr || H_out == nullptr || rstd == nullptr || dY == nullptr) return SBL_ERR_INVALID_ARG;
+    const bool reads_y = g_post != nullptr || dgate != nullptr;
+    if ((Y == nullptr && reads_y) || H_out == nullptr || rstd == nullptr || dY == nullptr) return SBL_ERR_INVALID_ARG;
     for (int i = 0; i < readers; ++i)
       if (dXn[i] == nullptr) return SBL_ERR_INVALID_ARG;
   }

@@ -48,7 +48,8 @@ def _bwd(cl, readers=1, n_ptr=None, **kw):
     (1, dict(readers=0)), (1, dict(readers=4)), (1, dict(dXn=None)), (1, dict(readers=2, n_ptr=[AL, None, AL, AL])),
     (1, dict(flags=8)), (1, dict(acc=2)), (1, dict(g_post=None)), (1, dict(dgate=AL)), (1, dict(s=math.inf)),
     (1, dict(Y=None)), (1, dict(H_out=None)), (1, dict(rstd=None)), (1, dict(dY=None)), (1, dict(ws=None)),
-    (1, dict(gate=AL, period=0)), (2, dict(T=-1)), (2, dict(d=8)), (2, dict(d=16400)),
+    (1, dict(gate=AL, period=0)),
+    (1, dict(Y=None, g_post=None, dg_post=None, gate=AL, period=2, dgate=AL)), (2, dict(T=-1)), (2, dict(d=8)), (2, dict(d=16400)),
     (3, dict(Y=AL + 8)), (3, dict(n_ptr=[AL + 4, AL, AL, AL])), (3, dict(ws=AL + 16)), (3, dict(dg_pre=AL + 4)),
     (5, dict(ws_bytes=16)),
 ])

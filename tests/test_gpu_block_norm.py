@@ -224,6 +224,24 @@ def test_accumulate_in_place_and_without_stream_gradient(lib, period):
     c.check_backward(with_dh=False)
 
 
+@pytest.mark.parametrize("period", [None, 3])
+def test_backward_without_y(lib, period):
+    """Neither a branch norm nor the gate's gradient: y is not read, and nothing else changes."""
+    c = Case(41, 304, post=False, period=period, seed=15)
+    c.buffers()
+    c.forward(lib)
+    c.backward(lib)
+    want = [c.dY.clone(), c.dH.clone(), c.grads["dg_pre"].clone()]
+    n = lib.sbl_block_norm_backward_workspace_bytes(304)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    c.dY.fill_(77)
+    c.dH.fill_(77)
+    lib.sbl_block_norm_backward(c.dXn, c.dH_out, None, c.H_out[:41], None, c.gate, period or 0, c.s, c.g_pre, c.rstd, 41,
+                                304, 0, c.dY, c.dH, None, c.grads["dg_pre"], None, 0, ws, n)
+    for a, b in zip(want, (c.dY, c.dH, c.grads["dg_pre"])):
+        assert torch.equal(a, b)
+
+
 def test_empty_batch(lib):
     e = torch.empty(0, 64, device="cuda")
     b = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
