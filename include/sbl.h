@@ -195,6 +195,8 @@ sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* works
  *              aligned).  n >= 0 elements, any n; a tensor of n = 0 is
  *              skipped.  out may be g itself (in place; with clip = 1 nothing
  *              is then written); it may not overlap any gradient otherwise.
+ *              A gradient that is listed twice counts twice, and may then
+ *              not be clipped in place.
  *              sbl_grad_norm_group ignores out.
  *   max_norm   > 0.
  *   sumsq      1 double out (device, 8-byte aligned).
@@ -328,7 +330,7 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
  *   gate       [ceil(T / gate_period), d] bf16 or NULL: token t takes row
  *              t / gate_period (1: a row for each token; >= T: one row for
  *              all).  gate_period >= 1, ignored without a gate.
- *   d          multiple of 16, at most 16384.  T >= 0.
+ *   d          multiple of 16, at most 16384.  0 <= T <= 2^30.
  *   H_out      [T, d] out, type of H; may be H itself.
  *   Xn         optional (NULL): [T, d] bf16 out (the input of the dW product).
  *   Xq, amax   optional, both or neither: [T, d] int8 and [T] float out.
@@ -353,6 +355,7 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
  *              neither g_post nor dgate is given.
  *   dY         [T, d] bf16 out (the dY of the branch's product).
  *   dH         optional (NULL): [T, d] out, type of H; may be dH_out itself.
+ *              No other output may overlap an input or another output.
  *   dg_post, dg_pre [d], dgate [rows of gate, d]: optional (NULL), float out;
  *              accumulate = 1 adds into the contents, 0 overwrites.
  *   workspace  device scratch of sbl_block_norm_backward_workspace_bytes(d)
@@ -475,7 +478,8 @@ sbl_status sbl_forward_sparse24(const int8_t* Xq, const float* amax, const uint8
  * scaling).
  *   Xq [T, d_in] int8, amax [T] float (sbl_act_quant, sbl_block_norm),
  *   Wq [d_out, d_in] int8, wmax [d_out] float; codes may take any int8 value.
- *   d_in >= 16, at most 131056 (int32 sums cannot overflow).
+ *   d_in >= 16, at most 131056 (int32 sums cannot overflow); T and d_out at
+ *   most 2^30.
  *   flags      SBL_W8A8_Y_BF16: Y is bf16, else float.
  *   Y          [T, d_out] out. */
 #define SBL_W8A8_Y_BF16 1u

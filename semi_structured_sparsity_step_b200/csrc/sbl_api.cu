@@ -94,7 +94,7 @@ const char* sbl_status_string(int status) {
   }
 }
 
-int sbl_version(void) { return 100; }
+int sbl_version(void) { return 101; }
 
 sbl_status sbl_set_gemm_variant(int variant) {
   if (variant != 0 && variant != 1) return SBL_ERR_INVALID_ARG;
@@ -305,10 +305,13 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
                                          d->num_sms));
 }
 
+// Rows that the launch arithmetic of the calls below counts in 32 bits.
+static constexpr int kMaxTokens = 1 << 30;
+
 static sbl_status check_block_norm(const void* g_pre, const void* gate, int gate_period, float res_scale, int T,
                                    int d, unsigned flags) {
   if ((flags & ~(SBL_BLOCK_Y_BF16 | SBL_BLOCK_H_F32)) != 0u) return SBL_ERR_INVALID_ARG;
-  if (T < 0 || d <= 0 || d % 16 != 0 || d > kBlockNormMaxWidth) return SBL_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens || d <= 0 || d % 16 != 0 || d > kBlockNormMaxWidth) return SBL_ERR_SHAPE;
   if (!std::isfinite(res_scale) || (gate != nullptr && gate_period < 1)) return SBL_ERR_INVALID_ARG;
   if (T > 0 && g_pre == nullptr) return SBL_ERR_INVALID_ARG;
   return SBL_OK;
@@ -452,7 +455,7 @@ sbl_status sbl_forward_w8a8(const int8_t* Xq, const float* amax, const int8_t* W
   if ((flags & ~SBL_W8A8_Y_BF16) != 0u) return SBL_ERR_INVALID_ARG;
   sbl_status st = check_dims(d_in, d_out);
   if (st != SBL_OK) return st;
-  if (T < 0 || d_in == 0 || d_in >= (1 << 17)) return SBL_ERR_SHAPE;
+  if (T < 0 || T > kMaxTokens || d_out > kMaxTokens || d_in == 0 || d_in >= (1 << 17)) return SBL_ERR_SHAPE;
   if (T == 0 || d_out == 0) return SBL_OK;
   if (Xq == nullptr || amax == nullptr || Wq == nullptr || wmax == nullptr || Y == nullptr)
     return SBL_ERR_INVALID_ARG;

@@ -101,11 +101,12 @@ class BlockNorm:
 
     def backward(self, dXn, dH_out, Y, dY, dH, gate=None, gate_period=0, dgate=None, accumulate=False, stream=None):
         """dXn: the gradients of Xn from each product that read it (1 to 3); the gains' gradients go
-        to dg_pre and dg_post.  Uses H_out and the factors of the last forward."""
+        to dg_pre and dg_post.  The tokens are those of the last forward, whose H_out and factors it
+        uses; Y may be None where nothing needs it (no g_post, no dgate)."""
         if self.ws is None:
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
         B.sbl_block_norm_backward(dXn, dH_out, Y, self.H_out, self.g_post, gate, gate_period, self.res_scale,
-                                  self.g_pre, self.rstd, Y.shape[0], self.d, self.flags, dY, dH, self.dg_post,
+                                  self.g_pre, self.rstd, dY.shape[0], self.d, self.flags, dY, dH, self.dg_post,
                                   self.dg_pre, dgate, int(accumulate), self.ws, self.ws_bytes, stream)
 
 

@@ -27,7 +27,7 @@ def _norm(cl, **kw):
     (1, dict(flags=4)), (1, dict(eps=0.0)), (1, dict(eps=math.nan)), (1, dict(s=math.inf)), (1, dict(s=math.nan)),
     (1, dict(gate=AL, period=0)), (1, dict(gate=AL, period=-1)), (1, dict(Y=None)), (1, dict(H=None)),
     (1, dict(H_out=None)), (1, dict(g_pre=None)), (1, dict(Xq=None)), (1, dict(amax=None)),
-    (2, dict(T=-1)), (2, dict(d=24)), (2, dict(d=0)), (2, dict(d=-16)), (2, dict(d=16400)),
+    (2, dict(T=-1)), (2, dict(T=2 ** 30 + 1)), (2, dict(d=24)), (2, dict(d=0)), (2, dict(d=-16)), (2, dict(d=16400)),
     (3, dict(Y=AL + 8)), (3, dict(H=AL + 4)), (3, dict(gate=AL + 2, period=1)), (3, dict(rstd=AL + 4)),
     (3, dict(Xn=AL + 8)), (0, dict(T=0)),
 ])
@@ -100,12 +100,12 @@ def test_binding_refuses_tensors_that_the_call_would_misread(monkeypatch):
     """A host tensor, a wrong type, a strided view and a short buffer never reach the library."""
     import torch
     from semi_structured_sparsity_step_b200 import _binding as B
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(B, "_device", lambda: 0)
     a = B._args("sbl_block_norm")
     assert a(None, torch.float32, 4) is None and a(AL, torch.float32, 4) == AL
     with pytest.raises(B.SblError):
         a(torch.zeros(4), torch.float32, 4)  # on the host
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # what get_device() gives for a host tensor
+    monkeypatch.setattr(B, "_device", lambda: -1)  # what get_device() gives for a host tensor
     a = B._args("sbl_block_norm")
     x = torch.zeros(4, 8)
     assert a(x, torch.float32, 32) == x.data_ptr()
@@ -117,7 +117,7 @@ def test_binding_refuses_tensors_that_the_call_would_misread(monkeypatch):
 
 @pytest.mark.parametrize("status,kw", [
     (1, dict(flags=2)), (1, dict(Xq=None)), (1, dict(amax=None)), (1, dict(Wq=None)), (1, dict(wmax=None)),
-    (1, dict(Y=None)), (2, dict(T=-1)), (2, dict(d_in=24)), (2, dict(d_in=0)), (2, dict(d_in=131072)),
+    (1, dict(Y=None)), (2, dict(T=-1)), (2, dict(T=2 ** 30 + 1)), (2, dict(d_out=2 ** 30 + 8)), (2, dict(d_in=24)), (2, dict(d_in=0)), (2, dict(d_in=131072)),
     (2, dict(d_out=12)), (2, dict(d_out=-8)), (3, dict(Xq=AL + 8)), (3, dict(wmax=AL + 4)), (3, dict(Y=AL + 2)),
     (0, dict(T=0)), (0, dict(d_out=0)),
 ])
