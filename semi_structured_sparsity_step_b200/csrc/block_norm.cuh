@@ -1,12 +1,12 @@
 // block_norm.cuh -- what the block norm's forward and backward kernels share: 4 neighbouring
-// columns in either type, the ring of rows that bulk copies keep ahead of the arithmetic, and the
-// dependent launch.
+// columns in either type, and the ring of rows that bulk copies keep ahead of the arithmetic.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
+#include "pdl.cuh"
 #include "sbl_device.cuh"
 
 namespace sbl {
@@ -78,33 +78,5 @@ __device__ __forceinline__ void lane_sync(int rib) {
   else
     asm volatile("bar.sync %0, %1;" ::"r"(rib + 1), "n"(TPR) : "memory");
 }
-
-// Programmatic dependent launch: a kernel may be set up while the previous one of its stream
-// finishes, and touches global memory only after wait().
-namespace pdl {
-
-__device__ __forceinline__ void wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch(void (*kern)(KArgs...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
-                   Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
-}
-
-}  // namespace pdl
 
 }  // namespace sbl

@@ -14,15 +14,20 @@
 // tiles up through distributed shared memory, each block a share of the token columns, by bulk
 // reductions into its shared memory (reading the other blocks' tiles word by word instead pays their
 // latency over and over: 28 us against 8 at 256 x 2048 x 2048 in four splits).  int32 sums are exact
-// in any order.  A warp writes 32 neighbouring outputs of a token.  Barriers, tensor memory and descriptors are set up while the previous kernel finishes
-// (programmatic dependent launch); global memory is touched only after it has.
+// in any order.  A warp writes 32 neighbouring outputs of a token.  Barriers, tensor memory and
+// descriptors are set up while the previous kernel finishes (programmatic dependent launch); global
+// memory is touched only after it has.
 // Every mbarrier wait is bounded (sbl_device.cuh).
+//
+// Measured: 1 x 11008 x 32768 (361 MB of weights) 55.6 us, the measured copy rate; 1 x 2048 x 11008
+// 6.3 us and 509 x 2048 x 2048 7.6 us with the operands in L2, of which about 3 us are the launch and
+// the first copy's latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 
-#include "block_norm.cuh"
+#include "pdl.cuh"
 #include "sbl_device.cuh"
 #include "sbl_internal.h"
 
@@ -173,7 +178,7 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
     for (int c0 = 0; c0 < cols; c0 += 32) {
       uint32_t r[32];
       tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(c0), r);
-      tmem_ld_wait();
+      tmem_ld_wait_for(r);
       if (cs == 1) {
         // every result before the first store: a store could alias the scales for all the compiler
         // knows, and each scale would wait for the store before it (65 cycles a column, measured)

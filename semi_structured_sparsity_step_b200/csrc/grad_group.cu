@@ -18,7 +18,7 @@
 #include <cuda_runtime.h>
 #include <cstdint>
 
-#include "sbl_device.cuh"
+#include "pdl.cuh"
 #include "sbl_internal.h"
 
 namespace sbl {
@@ -41,9 +41,6 @@ struct GradTable {
   int count;
   int in_place;  // every out is its g
 };
-
-__device__ __forceinline__ void gg_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void gg_pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 // L2 eviction priorities: `last` for what the scaling pass reads first, `first` for the rest.
 __device__ __forceinline__ uint64_t policy_last() {
@@ -139,8 +136,8 @@ __device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n
 __global__ void __launch_bounds__(kGgThreads) grad_sumsq_kernel(const __grid_constant__ GradTable tab,
                                                                 double* __restrict__ partial, unsigned keep) {
   __shared__ double scratch[kGgThreads / 32];
-  gg_pdl_wait();
-  gg_pdl_trigger();
+  pdl::wait();
+  asm volatile("griddepcontrol.launch_dependents;");
   const unsigned total = tab.tile_start[tab.count];
   const uint64_t last = policy_last(), first = policy_first();
   double s = 0.0;
@@ -179,7 +176,7 @@ __device__ __forceinline__ void store_norm(double S, float c, double* sumsq, flo
 __global__ void __launch_bounds__(kGgThreads) grad_norm_finish_kernel(const double* __restrict__ partial, int count,
                                                                       double* sumsq, float* norm) {
   __shared__ double scratch[kGgThreads / 32];
-  gg_pdl_wait();
+  pdl::wait();
   const double S = total_sumsq(partial, count, scratch);
   store_norm(S, 0.0f, sumsq, norm, nullptr);
 }
@@ -231,7 +228,7 @@ __global__ void __launch_bounds__(kGgThreads)
     grad_scale_kernel(const __grid_constant__ GradTable tab, const double* __restrict__ partial, int partials,
                       double max_norm, double* sumsq, float* norm, float* clip) {
   __shared__ double scratch[kGgThreads / 32];
-  gg_pdl_wait();
+  pdl::wait();
   const double S = total_sumsq(partial, partials, scratch);
   const float c = clip_factor(S, max_norm);
   if (sumsq != nullptr) store_norm(S, c, sumsq, norm, clip);
@@ -282,20 +279,6 @@ int fill_table(const GradTensorDev* t, int i, int count, GradTable& tab) {
   return i;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t gg_launch(void (*kern)(KArgs...), int grid, cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kGgThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
-}
-
 }  // namespace
 
 // One row of partial sums per launch of the norm pass; launches are cut by tensor count (and by
@@ -315,7 +298,7 @@ cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them,
     if (tab.count == 0) break;
     const unsigned total = tab.tile_start[tab.count];
     const int grid = static_cast<int>(total < static_cast<unsigned>(gg_blocks(num_sms)) ? total : gg_blocks(num_sms));
-    const cudaError_t e = gg_launch(grad_sumsq_kernel, grid, stream, tab, partial + used,
+    const cudaError_t e = pdl::launch(grad_sumsq_kernel, grid, kGgThreads, 0, 1, stream, tab, partial + used,
                                     clip_them ? kGgKeepTiles : 0u);
     if (e != cudaSuccess) return e;
     used += grid;
@@ -325,10 +308,10 @@ cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them,
     if (clip_them) {
       tab.count = 0;
       tab.tile_start[0] = 0;
-      return gg_launch(grad_scale_kernel, 1, stream, tab, static_cast<const double*>(partial), used, max_norm, sumsq,
+      return pdl::launch(grad_scale_kernel, 1, kGgThreads, 0, 1, stream, tab, static_cast<const double*>(partial), used, max_norm, sumsq,
                        norm, clip);
     }
-    return gg_launch(grad_norm_finish_kernel, 1, stream, static_cast<const double*>(partial), used, sumsq, norm);
+    return pdl::launch(grad_norm_finish_kernel, 1, kGgThreads, 0, 1, stream, static_cast<const double*>(partial), used, sumsq, norm);
   }
   bool first = true;
   for (int i = 0; i < count;) {
@@ -336,7 +319,7 @@ cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them,
     if (tab.count == 0) break;
     const unsigned total = tab.tile_start[tab.count];
     const int grid = static_cast<int>(total < static_cast<unsigned>(gg_blocks(num_sms)) ? total : gg_blocks(num_sms));
-    const cudaError_t e = gg_launch(grad_scale_kernel, grid, stream, tab, static_cast<const double*>(partial), used,
+    const cudaError_t e = pdl::launch(grad_scale_kernel, grid, kGgThreads, 0, 1, stream, tab, static_cast<const double*>(partial), used,
                                     max_norm, first ? sumsq : static_cast<double*>(nullptr), norm, clip);
     if (e != cudaSuccess) return e;
     first = false;
