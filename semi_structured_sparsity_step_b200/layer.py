@@ -111,19 +111,31 @@ class BlockNorm:
 
 
 class Int8Linear:
-    """A projection held in 8 bits: W [d_out, d_in] bf16, quantised row by row once."""
+    """A projection held in 8 bits: W [d_out, d_in] bf16, quantised row by row.
+
+    weight_step() quantises W again after it has changed.  backward() is the
+    straight-through estimator on the bf16 W: dX = dY . W, dW = dY^T . X."""
 
     def __init__(self, W: torch.Tensor):
         assert W.is_cuda and W.dtype == torch.bfloat16 and W.is_contiguous()
+        self.W = W
         self.d_out, self.d_in = W.shape
         self.Wq = torch.empty(self.d_out, self.d_in, dtype=torch.int8, device=W.device)
         self.wmax = torch.empty(self.d_out, dtype=torch.float32, device=W.device)
-        B.sbl_act_quant(W, self.d_out, self.d_in, self.Wq, self.wmax)
+        self.one = torch.ones(1, dtype=torch.float32, device=W.device)
+        self.weight_step()
+
+    def weight_step(self, stream=None):
+        B.sbl_act_quant(self.W, self.d_out, self.d_in, self.Wq, self.wmax, stream)
 
     def forward(self, Xq, amax, Y, stream=None):
         """Y [T, d_out] in fp32 or bf16, by its type."""
         flags = B.SBL_W8A8_Y_BF16 if Y.dtype == torch.bfloat16 else 0
         B.sbl_forward_w8a8(Xq, amax, self.Wq, self.wmax, Xq.shape[0], self.d_in, self.d_out, flags, Y, stream)
+
+    def backward(self, dY, X, dX, dW, accumulate_dW=False, stream=None):
+        B.sbl_backward(dY, X, self.W, self.one, dY.shape[0], self.d_in, self.d_out, dX, dW, int(accumulate_dW), None,
+                       0, stream)
 
 
 class GradClip:

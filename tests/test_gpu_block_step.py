@@ -91,6 +91,34 @@ def test_training_step(lib):
     assert np.array_equal(L1.W_eff.cpu().numpy(), step["weff"])
 
 
+def test_int8_projection_trains(lib):
+    """Forward in 8 bits, the straight-through gradients, an update of W and its new codes."""
+    from semi_structured_sparsity_step_b200.layer import Int8Linear, act_quant
+    T, d_in, d_out = 77, 272, 136
+    w, x, dy = synth.normal_weight(d_out, d_in, seed=55), synth.activations(T, d_in, seed=56), \
+        synth.grad_output(T, d_out, seed=57)
+    L = Int8Linear(w.cuda())
+    dev = dict(device="cuda")
+    X, Xq, amax = x.cuda(), torch.empty(T, d_in, dtype=torch.int8, **dev), torch.empty(T, **dev)
+    Y, dX, dW = torch.empty(T, d_out, **dev), torch.empty(T, d_in, **dev), torch.empty(d_out, d_in, **dev)
+    act_quant(X, Xq, amax)
+    L.forward(Xq, amax, Y)
+    L.backward(dy.cuda(), X, dX, dW)
+    lib.sbl_check()
+    xq, am = oracle.act_quant(synth.bits(x))
+    wq, wm = oracle.act_quant(synth.bits(w))
+    assert np.array_equal(_f(Y), oracle.w8a8_out(oracle.forward_acc(xq, wq), am, wm))
+    # dX = dY W: the oracle's product with W in the ternary weight's place and gamma = 1
+    wf = w.float().numpy().astype(np.float64)
+    ref = oracle.bf16_to_f32(synth.bits(dy)).astype(np.float64) @ wf
+    check_bwd(_f(dX), ref, np.abs(oracle.bf16_to_f32(synth.bits(dy))).astype(np.float64) @ np.abs(wf), "dX")
+    check_bwd(_f(dW), oracle.backward_dw(synth.bits(dy), synth.bits(x)), abs_dw(synth.bits(dy), synth.bits(x)), "dW")
+    L.W.sub_((0.01 * dW).to(torch.bfloat16))
+    L.weight_step()
+    wq, wm = oracle.act_quant(synth.bits(L.W.cpu()))
+    assert np.array_equal(L.Wq.cpu().numpy(), wq) and np.array_equal(L.wmax.cpu().numpy(), wm)
+
+
 @pytest.mark.parametrize("batch", [1, 5])
 def test_decode_step_in_a_graph(lib, batch):
     """Packed ternary projection, block norm, 8-bit head: one graph, replayed on new inputs."""
