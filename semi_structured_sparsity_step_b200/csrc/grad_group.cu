@@ -10,9 +10,9 @@
 // and writes them once, where the floor is one read and one write.  Two launches: the first
 // leaves one fp64 partial sum per block, the second sums the partials (every block, in the
 // same order, so no block waits for another) and scales.  The scaling pass walks the tiles
-// backwards, so it starts with what the norm pass read last and asked L2 to hold; gradients that fit
+// backwards, so it starts with what the norm pass read last and left in L2; gradients that fit
 // there are read from HBM once.  No atomics: S is the same bits for the same tensors on every run on
-// one device.  Measured: norm pass alone 176 us for 1233 MB (7.0 TB/s), with clipping 586 us, where
+// one device.  Measured: norm pass alone 173 us for 1233 MB (7.1 TB/s), with clipping 593 us, where
 // reading all but 64 MB twice and writing once takes 555 us at the measured copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -27,8 +27,9 @@ namespace {
 constexpr int kGgThreads = 256;
 constexpr int kGgVecs = 4;                            // 16-byte vectors per thread and tile
 constexpr int kGgTileVecs = kGgThreads * kGgVecs;     // 16 KB per tile
-// The scaling pass is asked to find this much of the norm pass's last reads in L2.  Measured on
-// gradients of 1233 MB: 586 us with 48 to 96 MB, 591 with none, 596 with plain loads.
+// The scaling pass is to find this much of the norm pass's last reads in L2; what is read before goes
+// first.  Measured on gradients of 308 MB: 144.5 us, with 32 or 128 MB 147.6, with plain loads 152.5;
+// on 1233 MB 593, 597 and 596.
 constexpr unsigned kGgKeepTiles = (64u << 20) / (kGgTileVecs * 16);
 constexpr int kGgTensors = 128;                       // tensors per launch (the table is a kernel parameter)
 
@@ -42,10 +43,11 @@ struct GradTable {
   int in_place;  // every out is its g
 };
 
-// L2 eviction priorities: `last` for what the scaling pass reads first, `first` for the rest.
-__device__ __forceinline__ uint64_t policy_last() {
+// L2 eviction priorities: normal for what the scaling pass reads first, `first` for the rest (not
+// evict_last: below the limit nothing reads those lines again, and they would stay).
+__device__ __forceinline__ uint64_t policy_normal() {
   uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
 __device__ __forceinline__ uint64_t policy_first() {
@@ -139,13 +141,13 @@ __global__ void __launch_bounds__(kGgThreads) grad_sumsq_kernel(const __grid_con
   pdl::wait();
   asm volatile("griddepcontrol.launch_dependents;");
   const unsigned total = tab.tile_start[tab.count];
-  const uint64_t last = policy_last(), first = policy_first();
+  const uint64_t normal = policy_normal(), first = policy_first();
   double s = 0.0;
   TileCursor c{0};
   for (unsigned t = blockIdx.x; t < total; t += gridDim.x) {
     c.seek(tab, t);
     const unsigned long long v0 = static_cast<unsigned long long>(t - tab.tile_start[c.p]) * kGgTileVecs;
-    const uint64_t pol = total - t <= keep ? last : first;
+    const uint64_t pol = total - t <= keep ? normal : first;
     s = ((tab.bf16[c.p >> 5] >> (c.p & 31)) & 1u) ? tile_sumsq<true>(tab.g[c.p], tab.n[c.p], v0, s, pol)
                                                   : tile_sumsq<false>(tab.g[c.p], tab.n[c.p], v0, s, pol);
   }
