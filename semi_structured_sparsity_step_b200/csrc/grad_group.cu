@@ -12,7 +12,7 @@
 // same order, so no block waits for another) and scales.  The scaling pass walks the tiles
 // backwards, so it starts with what the norm pass read last and left in L2; gradients that fit
 // there are read from HBM once.  No atomics: S is the same bits for the same tensors on every run on
-// one device.  Measured: norm pass alone 173 us for 1233 MB (7.1 TB/s), with clipping 593 us, where
+// one device.  Measured: norm pass alone 173 us for 1233 MB (7.1 TB/s), with clipping 550 us, where
 // reading all but 64 MB twice and writing once takes 555 us at the measured copy rate.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,8 +28,8 @@ constexpr int kGgThreads = 256;
 constexpr int kGgVecs = 4;                            // 16-byte vectors per thread and tile
 constexpr int kGgTileVecs = kGgThreads * kGgVecs;     // 16 KB per tile
 // The scaling pass is to find this much of the norm pass's last reads in L2; what is read before goes
-// first.  Measured on gradients of 308 MB: 144.5 us, with 32 or 128 MB 147.6, with plain loads 152.5;
-// on 1233 MB 593, 597 and 596.
+// first.  Measured on gradients of 308 MB: 144.5 us, with 32 or 128 MB 147.6, with plain loads 152.5
+// (136.8 with the scaling pass as it is now).
 constexpr unsigned kGgKeepTiles = (64u << 20) / (kGgTileVecs * 16);
 constexpr int kGgTensors = 128;                       // tensors per launch (the table is a kernel parameter)
 
@@ -251,6 +251,11 @@ __global__ void __launch_bounds__(kGgThreads)
 }
 
 constexpr int kGgBlocksPerSm = 4;
+// Tiles per block of the scaling pass.  Blocks that come one after the other walk the memory more evenly
+// than four per SM that stay: 1233 MB 550 us against 593 (6.4 against 5.7 TB/s of that pass); a block
+// reads the partial sums (5 KB, in L2) for two tiles.  In place the blocks stay: below the limit there
+// is nothing to scale, and 38000 blocks that find that out take 50 us, 592 take 3.
+constexpr unsigned kGgScaleTiles = 2;
 constexpr int kGgMaxBlocks = 1024;  // of one launch: sizes the workspace
 
 int gg_blocks(int num_sms) {
@@ -320,7 +325,9 @@ cudaError_t launch_grad_group(const GradTensorDev* t, int count, bool clip_them,
     i = fill_table(t, i, count, tab);
     if (tab.count == 0) break;
     const unsigned total = tab.tile_start[tab.count];
-    const int grid = static_cast<int>(total < static_cast<unsigned>(gg_blocks(num_sms)) ? total : gg_blocks(num_sms));
+    const unsigned blocks = (total + kGgScaleTiles - 1) / kGgScaleTiles;
+    const unsigned stay = static_cast<unsigned>(gg_blocks(num_sms));
+    const int grid = static_cast<int>(tab.in_place != 0 && blocks > stay ? stay : blocks);
     const cudaError_t e = pdl::launch(grad_scale_kernel, grid, kGgThreads, 0, 1, stream, tab, static_cast<const double*>(partial), used,
                                     max_norm, first ? sumsq : static_cast<double*>(nullptr), norm, clip);
     if (e != cudaSuccess) return e;
