@@ -277,3 +277,49 @@ def test_clip_past_2_32_elements(lib):
     assert c.item() == pytest.approx(float(factor), rel=2.0 ** -23)
     want = torch.tensor([3.0 * c.item(), 2.0 ** -17 * c.item()]).to(torch.bfloat16).cuda()
     assert g[-1] == want[0] and torch.all(g[:-1] == want[1])
+
+
+def test_stream_argument_and_refused_tensors(lib):
+    """Every call takes a stream, as an object or a handle; tensors that it would misread are refused
+    before a launch."""
+    T, d = 37, 256
+    dev = dict(device="cuda")
+    Y, H = torch.randn(T, d, **dev), torch.randn(T, d, **dev).to(torch.bfloat16)
+    gain = torch.ones(d, dtype=torch.bfloat16, **dev)
+    W, wmax = torch.ones(64, d, dtype=torch.int8, **dev), torch.ones(64, **dev)
+    n = lib.sbl_block_norm_backward_workspace_bytes(d)
+    ws = torch.empty(n, dtype=torch.uint8, **dev)
+
+    def run(stream):
+        o = dict(h=torch.zeros_like(H), xq=torch.zeros(T, d, dtype=torch.int8, **dev), am=torch.zeros(T, **dev),
+                 r=torch.zeros(2 * T, **dev), out=torch.zeros(T, 64, **dev), dY=torch.zeros_like(H),
+                 dg=torch.zeros(d, **dev), s=torch.zeros(1, dtype=torch.float64, **dev), c=torch.zeros(d, **dev))
+        torch.cuda.synchronize()  # the buffers were filled on the current stream
+        lib.sbl_block_norm(Y, H, gain, None, 0, 1.0, gain, 1e-6, T, d, 0, o["h"], None, o["xq"], o["am"], o["r"], stream)
+        lib.sbl_forward_w8a8(o["xq"], o["am"], W, wmax, T, d, 64, 0, o["out"], stream)
+        lib.sbl_block_norm_backward([Y], None, Y, o["h"], gain, None, 0, 1.0, gain, o["r"], T, d, 0, o["dY"], None,
+                                    o["dg"], None, None, 0, ws, n, stream)
+        lib.sbl_grad_clip_group([(o["dg"], o["c"], d, False)], 1.0, o["s"], None, None, ws, n, stream)
+        torch.cuda.synchronize()
+        return o
+
+    side = torch.cuda.Stream()
+    want = run(None)
+    for stream in (side, side.cuda_stream):
+        got = run(stream)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+    o = want
+    bad = [torch.zeros(T, d), Y.to(torch.bfloat16), Y.t().contiguous().t(), Y[:-1]]  # host, type, strides, size
+    for b in bad:
+        with pytest.raises(lib.SblError):
+            lib.sbl_block_norm(b, H, gain, None, 0, 1.0, gain, 1e-6, T, d, 0, o["h"], None, o["xq"], o["am"], o["r"])
+        with pytest.raises(lib.SblError):
+            lib.sbl_block_norm_backward([b], None, Y, o["h"], gain, None, 0, 1.0, gain, o["r"], T, d, 0, o["dY"], None,
+                                        o["dg"], None, None, 0, ws, n)
+        with pytest.raises(lib.SblError):
+            lib.sbl_grad_clip_group([(b, Y, T * d, False)], 1.0, o["s"], None, None, ws, n)
+        with pytest.raises(lib.SblError):
+            lib.sbl_forward_w8a8(o["xq"], o["am"], W, wmax, T, d, 64, 0, b[:, :64])
+    with pytest.raises(lib.SblError):  # a workspace shorter than it is said to be
+        lib.sbl_grad_clip_group([(Y, Y, T * d, False)], 1.0, o["s"], None, None, ws[:64], n)
+    lib.sbl_check()
