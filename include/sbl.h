@@ -194,9 +194,10 @@ sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* works
  *              returns; the pointers inside are device pointers, 16-byte
  *              aligned).  n >= 0 elements, any n; a tensor of n = 0 is
  *              skipped.  out may be g itself (in place; with clip = 1 nothing
- *              is then written); it may not overlap any gradient otherwise.
- *              A gradient that is listed twice counts twice, and may then
- *              not be clipped in place.
+ *              is then written); it may not overlap any other tensor's g or
+ *              out (the same pointer is refused, SBL_ERR_INVALID_ARG).  A
+ *              gradient that is listed twice counts twice, and can then not
+ *              be clipped in place.
  *              sbl_grad_norm_group ignores out.
  *   max_norm   > 0.
  *   sumsq      1 double out (device, 8-byte aligned).

@@ -207,6 +207,33 @@ sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* works
 
 size_t sbl_grad_group_workspace_bytes(int count) { return count < 0 ? 0 : grad_group_workspace_bytes(count); }
 
+// Whether a clipped gradient would be written where another tensor's is written or read: with the blocks of
+// one launch on both, the result would depend on their order.  A hash table of the out pointers (a sort
+// of a few hundred tensors takes longer than the launches).
+static bool outs_collide(const sbl_grad_tensor* t, int count) {
+  size_t size = 16;
+  while (size < 2 * static_cast<size_t>(count)) size *= 2;
+  std::vector<int> slots(size, -1);
+  // the slot that holds out == p, or the free one where it would go
+  auto find = [&](const void* p) {
+    size_t h = static_cast<size_t>((reinterpret_cast<uintptr_t>(p) >> 4) * 0x9E3779B97F4A7C15ull >> 20) & (size - 1);
+    while (slots[h] >= 0 && t[slots[h]].out != p) h = (h + 1) & (size - 1);
+    return h;
+  };
+  for (int i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const size_t h = find(t[i].out);
+    if (slots[h] >= 0) return true;
+    slots[h] = i;
+  }
+  for (int i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const size_t h = find(t[i].g);
+    if (slots[h] >= 0 && slots[h] != i) return true;
+  }
+  return false;
+}
+
 static sbl_status grad_group(const sbl_grad_tensor* tensors, int count, bool clip_them, double max_norm,
                              double* sumsq, float* norm, float* clip, void* workspace, size_t workspace_bytes,
                              void* stream) {
@@ -225,10 +252,11 @@ static sbl_status grad_group(const sbl_grad_tensor* tensors, int count, bool cli
       (reinterpret_cast<uintptr_t>(clip) & 3u) != 0 || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return SBL_ERR_ALIGN;
   if (workspace_bytes < grad_group_workspace_bytes(count)) return SBL_ERR_WORKSPACE;
-  DeviceInfo* d = nullptr;
-  const sbl_status st = current_device(&d);
-  if (st != SBL_OK) return st;
   try {
+    if (clip_them && outs_collide(tensors, count)) return SBL_ERR_INVALID_ARG;
+    DeviceInfo* d = nullptr;
+    const sbl_status st = current_device(&d);
+    if (st != SBL_OK) return st;
     std::vector<GradTensorDev> dev(static_cast<size_t>(count));
     for (int i = 0; i < count; ++i)
       dev[i] = GradTensorDev{tensors[i].g, tensors[i].out, tensors[i].n, tensors[i].bf16 != 0};

@@ -125,3 +125,17 @@ def test_forward_w8a8_refuses(cl, status, kw):
     a = dict(Xq=AL, amax=AL, Wq=AL, wmax=AL, T=4, d_in=32, d_out=16, flags=0, Y=AL)
     a.update(kw)
     assert cl.sbl_forward_w8a8(*a.values(), None) == status
+
+
+B2 = AL + 4096
+
+
+@pytest.mark.parametrize("tensors", [
+    [(AL, AL, 4, 0, 0), (AL, AL, 4, 0, 0)],              # clipped twice in place
+    [(AL, AL, 4, 0, 0), (AL, B2, 4, 0, 0)],              # read while it is clipped in place
+    [(AL, B2, 4, 0, 0), (AL + 64, B2, 4, 1, 0)],         # one output for two
+    [(AL, B2, 4, 0, 0), (B2, B2 + 64, 4, 0, 0)],         # the output of one is the gradient of another
+    [(AL + 64 * i, AL + 64 * i, 4, 0, 0) for i in range(300)] + [(AL + 64 * 7, B2 * 64, 4, 0, 0)],
+])
+def test_grad_clip_group_refuses_outputs_that_race(cl, tensors):
+    assert _clip(cl, tensors) == 1

@@ -173,3 +173,15 @@ def test_group_norm_feeds_the_optimizer_step(lib):
     ref = oracle.adamw_weight_step(synth.bits(w), dw.numpy(), m0.numpy(), v0.numpy(), 6, 8,
                                    oracle.adamw_scalars(1e-3, 0.9, 0.95, 1e-5, 0.1, 1), c)
     assert np.array_equal(synth.bits(W.cpu()), ref["w_bits"]) and np.array_equal(weff.cpu().numpy(), ref["weff"])
+
+
+def test_a_gradient_listed_twice_counts_twice(lib):
+    sizes, kinds = [4097, 4097, 5], [False, False, True]
+    a, b = _grads([4097, 5], [False, True], seed=77)
+    bufs, outs = [a, a, b], [torch.full_like(x, 7.0) for x in (a, a, b)]
+    c = Clip(lib, 3)
+    tensors = [(g, o, n, k) for g, o, n, k in zip(bufs, outs, sizes, kinds)]
+    c(tensors, 0.25)
+    _check(c, bufs, outs, sizes, kinds, 0.25)
+    with pytest.raises(lib.SblError):
+        c([(a, a, 4097, False), (a, a, 4097, False)], 0.25)
