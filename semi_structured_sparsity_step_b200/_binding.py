@@ -313,6 +313,11 @@ def _gate_count(gate, gate_period, T):
     return 0 if gate is None or gate_period < 1 else -(-T // gate_period)
 
 
+def _period(gate_period):
+    """The period as the library's int holds it: ctypes would cut 2^32 + 1 down to 1, and T is below 2^31."""
+    return min(gate_period, 0x7FFFFFFF)
+
+
 def sbl_block_norm(Y, H, g_post, gate, gate_period, res_scale, g_pre, eps, T, d, flags, H_out, Xn, Xq, amax, rstd,
                    stream=None) -> None:
     a = _args("sbl_block_norm")
@@ -320,9 +325,9 @@ def sbl_block_norm(Y, H, g_post, gate, gate_period, res_scale, g_pre, eps, T, d,
     f32, bf16 = torch.float32, torch.bfloat16
     yt, ht, n = bf16 if flags & SBL_BLOCK_Y_BF16 else f32, f32 if flags & SBL_BLOCK_H_F32 else bf16, T * d
     _call("sbl_block_norm", a(Y, yt, n), a(H, ht, n), a(g_post, bf16, d),
-          a(gate, bf16, _gate_count(gate, gate_period, T) * d), gate_period, res_scale, a(g_pre, bf16, d), eps, T, d,
-          flags, a(H_out, ht, n), a(Xn, bf16, n), a(Xq, torch.int8, n), a(amax, f32, T), a(rstd, f32, 2 * T),
-          _stream(stream))
+          a(gate, bf16, _gate_count(gate, gate_period, T) * d), _period(gate_period), res_scale, a(g_pre, bf16, d),
+          eps, T, d, flags, a(H_out, ht, n), a(Xn, bf16, n), a(Xq, torch.int8, n), a(amax, f32, T),
+          a(rstd, f32, 2 * T), _stream(stream))
 
 
 def sbl_block_norm_backward_workspace_bytes(d) -> int:
@@ -339,9 +344,9 @@ def sbl_block_norm_backward(dXn, dH_out, Y, H_out, g_post, gate, gate_period, re
     rows = _gate_count(gate, gate_period, T)
     readers = (_vp * max(1, len(dXn)))(*[a(x, f32, n) for x in dXn])
     _call("sbl_block_norm_backward", ctypes.addressof(readers), len(dXn), a(dH_out, ht, n), a(Y, yt, n),
-          a(H_out, ht, n), a(g_post, bf16, d), a(gate, bf16, rows * d), gate_period, res_scale, a(g_pre, bf16, d),
-          a(rstd, f32, 2 * T), T, d, flags, a(dY, bf16, n), a(dH, ht, n), a(dg_post, f32, d), a(dg_pre, f32, d),
-          a(dgate, f32, rows * d), int(accumulate),
+          a(H_out, ht, n), a(g_post, bf16, d), a(gate, bf16, rows * d), _period(gate_period), res_scale,
+          a(g_pre, bf16, d), a(rstd, f32, 2 * T), T, d, flags, a(dY, bf16, n), a(dH, ht, n),
+          a(dg_post, f32, d), a(dg_pre, f32, d), a(dgate, f32, rows * d), int(accumulate),
           a(workspace, torch.uint8, workspace_bytes), workspace_bytes, _stream(stream))
 
 

@@ -91,18 +91,21 @@ class BlockNorm:
         self.dg_post = torch.zeros(d, dtype=torch.float32, device=dev) if g_post is not None else None
         self.ws_bytes = B.sbl_block_norm_backward_workspace_bytes(d)
         self.ws = None  # allocated by the first backward
+        self.T = None  # tokens of the last forward
 
     def forward(self, Y, H, gate=None, gate_period=0, stream=None):
         """-> (H_out, Xn, Xq, amax) of the call's tokens."""
         T = Y.shape[0]
         B.sbl_block_norm(Y, H, self.g_post, gate, gate_period, self.res_scale, self.g_pre, self.eps, T, self.d,
                          self.flags, self.H_out, self.Xn, self.Xq, self.amax, self.rstd, stream)
+        self.T = T
         return self.H_out[:T], self.Xn[:T], self.Xq[:T], self.amax[:T]
 
     def backward(self, dXn, dH_out, Y, dY, dH, gate=None, gate_period=0, dgate=None, accumulate=False, stream=None):
         """dXn: the gradients of Xn from each product that read it (1 to 3); the gains' gradients go
         to dg_pre and dg_post.  The tokens are those of the last forward, whose H_out and factors it
         uses; Y may be None where nothing needs it (no g_post, no dgate)."""
+        assert dY.shape[0] == self.T  # the factors lie as that many tokens left them
         if self.ws is None:
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
         B.sbl_block_norm_backward(dXn, dH_out, Y, self.H_out, self.g_post, gate, gate_period, self.res_scale,
@@ -126,7 +129,9 @@ class Int8Linear:
         self.weight_step()
 
     def weight_step(self, stream=None):
-        B.sbl_act_quant(self.W, self.d_out, self.d_in, self.Wq, self.wmax, stream)
+        a = B._args("sbl_act_quant")
+        B.sbl_act_quant(a(self.W, torch.bfloat16, self.d_out * self.d_in), self.d_out, self.d_in, self.Wq, self.wmax,
+                        stream)
 
     def forward(self, Xq, amax, Y, stream=None):
         """Y [T, d_out] in fp32 or bf16, by its type."""
@@ -134,8 +139,13 @@ class Int8Linear:
         B.sbl_forward_w8a8(Xq, amax, self.Wq, self.wmax, Xq.shape[0], self.d_in, self.d_out, flags, Y, stream)
 
     def backward(self, dY, X, dX, dW, accumulate_dW=False, stream=None):
-        B.sbl_backward(dY, X, self.W, self.one, dY.shape[0], self.d_in, self.d_out, dX, dW, int(accumulate_dW), None,
-                       0, stream)
+        """dY, X: bf16, of one number of tokens; dX, dW: float out, each may be None."""
+        T, a = dY.shape[0], B._args("sbl_backward")
+        f32, bf16 = torch.float32, torch.bfloat16
+        n = self.d_out * self.d_in
+        B.sbl_backward(a(dY, bf16, T * self.d_out), a(X, bf16, T * self.d_in), a(self.W, bf16, n), self.one, T,
+                       self.d_in, self.d_out, a(dX, f32, T * self.d_in), a(dW, f32, n), int(accumulate_dW), None, 0,
+                       stream)
 
 
 class GradClip:

@@ -139,3 +139,52 @@ B2 = AL + 4096
 ])
 def test_grad_clip_group_refuses_outputs_that_race(cl, tensors):
     assert _clip(cl, tensors) == 1
+
+
+@pytest.mark.parametrize("period", [5, 2 ** 31 - 1, 2 ** 32 + 1, 2 ** 63 - 1])
+def test_gate_period_reaches_the_library_whole(monkeypatch, period):
+    """One gate row for all tokens, whatever the period beyond them: never cut down to an int of fewer bits."""
+    import torch
+    from semi_structured_sparsity_step_b200 import _binding as B
+    calls = []
+    monkeypatch.setattr(B, "_torch", torch)
+    monkeypatch.setattr(B, "_device", lambda: -1)  # what get_device() gives for a host tensor
+    monkeypatch.setattr(B, "_call", lambda name, *args: calls.append(args))
+    T, d = 5, 32
+    Y, H, gain = torch.zeros(T, d), torch.zeros(T, d, dtype=torch.bfloat16), torch.ones(1, d, dtype=torch.bfloat16)
+    B.sbl_block_norm(Y, H, None, gain, period, 1.0, gain, 1e-6, T, d, 0, H, None, None, None, None, 0)
+    B.sbl_block_norm_backward([Y], None, None, H, None, gain, period, 1.0, gain, Y, T, d, 0, H, None, None, None, None,
+                              0, None, 0, 0)
+    assert [ctypes.c_int(c[i]).value for c, i in zip(calls, (4, 7))] == [min(period, 2 ** 31 - 1)] * 2
+
+
+def test_layers_refuse_what_their_calls_would_misread(monkeypatch):
+    """A tensor of another device, type or size, and a backward of another number of tokens."""
+    import torch
+    from semi_structured_sparsity_step_b200 import _binding as B
+    from semi_structured_sparsity_step_b200 import layer
+    monkeypatch.setattr(B, "_torch", torch)
+    monkeypatch.setattr(B, "_call", lambda *args: None)
+    bf16 = torch.bfloat16
+    L = object.__new__(layer.Int8Linear)
+    L.W, L.d_out, L.d_in = torch.zeros(16, 32, dtype=bf16), 16, 32
+    L.Wq, L.wmax, L.one = torch.zeros(16, 32, dtype=torch.int8), torch.zeros(16), torch.ones(1)
+    good = dict(dY=torch.zeros(4, 16, dtype=bf16), X=torch.zeros(4, 32, dtype=bf16), dX=torch.zeros(4, 32),
+                dW=torch.zeros(16, 32))
+    monkeypatch.setattr(B, "_device", lambda: 0)  # the host tensors are not there
+    with pytest.raises(B.SblError):
+        L.weight_step(0)
+    with pytest.raises(B.SblError):
+        L.backward(**good, stream=0)
+    monkeypatch.setattr(B, "_device", lambda: -1)
+    L.weight_step(0)
+    L.backward(**good, stream=0)
+    L.backward(**dict(good, dX=None), stream=0)
+    for k, bad in (("dY", torch.zeros(4, 16)), ("X", good["X"][:3]), ("dX", good["dX"].to(bf16)),
+                   ("dW", torch.zeros(32, 16).t())):
+        with pytest.raises(B.SblError):
+            L.backward(**dict(good, **{k: bad}), stream=0)
+    N = object.__new__(layer.BlockNorm)
+    N.T = 4
+    with pytest.raises(AssertionError):
+        N.backward([good["dX"]], None, None, good["X"][:3], None, stream=0)
