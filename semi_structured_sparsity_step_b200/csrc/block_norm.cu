@@ -99,8 +99,9 @@ __device__ __forceinline__ double sum_squares(const float2 (&x)[VPT][2]) {
 }
 
 constexpr int bn_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
-// Resident blocks per SM: what the registers of VPT vectors per thread leave room for.
-constexpr int bn_blocks(int tpr, int vpt) { return tpr > 256 ? 1 : vpt == 8 ? 2 : vpt == 4 ? 3 : 4; }
+// Resident blocks per SM: what the registers of VPT vectors per thread leave room for (one more spills: of
+// 6 vectors, 1536 columns, 77 us against 68; of 3 vectors, 384 columns, 80 against 75).
+constexpr int bn_blocks(int tpr, int vpt) { return tpr > 256 ? 1 : vpt >= 5 ? 2 : vpt >= 3 ? 3 : 4; }
 
 template <int TPR, int VPT, bool YB, bool HF>
 __global__ void __launch_bounds__(bn_threads(TPR), bn_blocks(TPR, VPT)) block_norm_kernel(const BlockNormArgs a) {
@@ -278,49 +279,73 @@ cudaError_t run(BlockNormArgs a, cudaStream_t stream, int num_sms) {
   return pdl::launch(kern, static_cast<int>(blocks), THREADS, smem, 1, stream, a);
 }
 
-// Threads per row and columns per thread.  Few rows want many threads per row (latency), many rows few
-// (what every thread does once per row, the sums and two square roots, is shared by more columns).
+// Threads per row and vectors per thread.  Few rows want many threads per row (latency), many rows few
+// (what every thread does once per row, the sums and two square roots, is shared by more columns), and as
+// many vectors as the width fills: a vector past the row's end costs what a full one costs.
 // Measured, this choice against the other side of each rule, y fp32 and h bf16 unless said:
-//   32 threads (few rows: 2 vectors each) against 8 of 8: 256 columns, 16000 rows 14.0 us against 15.9,
-//     60000 rows 42.2 against 33.8;
+//   many rows, vectors by the width against always 8 (4 with an fp32 stream), 67 MB of y each: 528 columns
+//     79.6 us against 110, 1040 79.3 against 108, 1280 66 against 86, 2064 82 against 112, 5120 68 against 81;
+//   an fp32 stream: 5 vectors of the narrower shape against 3 of the wider: 528 columns 79.3 us against
+//     98.5, 1280 72.5 against 83.6; beyond 5 they leave the ring too shallow: 2048 columns, 16000 rows
+//     79.3 with 64 threads of 8 against 72.5 with 128 of 4;
+//   8 or 16 threads against 32: 128 columns, 8192 rows 7.1 us, 32768 rows 14.5 against 21.6, 131072 rows
+//     37 against 78; 272 columns, 15420 rows 16.8 against 15.8, 61680 rows 41.8 against 50.6;
+//     512 columns, 65536 rows 66.5 with 16 of 8 against 64.0 with 32 of 4;
 //   896 columns: 1 row 2.4 us with 256 threads, 2.6 with 128; 1000 rows 4.4 with 128, 5.9 with 4 vectors
-//     each; 16000 rows 31.5 with 32 of 8, 35.1 with 64 of 4;
+//     each; 16000 rows 31.5 with 32 of 7, 35.1 with 64 of 4;
 //   2048 columns: 300 rows 3.7 us with 256 threads, 4.5 with 64 of 8; 16000 rows 60.3 with 64 of 8,
-//     68.5 with 128 of 4; with an fp32 stream 79.3 against 72.5 (8 vectors leave the ring too shallow);
+//     68.5 with 128 of 4;
 //   4096 columns: 300 rows 4.7 us with 256 of 4, 5.6 with 128 of 8; 16000 rows 126 against 117;
 //   8192 columns: 300 rows 8.1 us with 256 of 8, 9.9 with 512 of 4; 1 row 4.2 against 4.0.
+
+// 5 to 8 vectors for rows of more than 4 TPR vectors.
+template <int TPR, bool YB, bool HF>
+cudaError_t run_wide(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
+  if (a.nv <= 5 * TPR) return run<TPR, 5, YB, HF>(a, stream, num_sms);
+  if (a.nv <= 6 * TPR) return run<TPR, 6, YB, HF>(a, stream, num_sms);
+  if (a.nv <= 7 * TPR) return run<TPR, 7, YB, HF>(a, stream, num_sms);
+  return run<TPR, 8, YB, HF>(a, stream, num_sms);
+}
+
+// 3 or 4 vectors for rows of more than 2 TPR.
+template <int TPR, bool YB, bool HF>
+cudaError_t run_narrow(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
+  return a.nv <= 3 * TPR ? run<TPR, 3, YB, HF>(a, stream, num_sms) : run<TPR, 4, YB, HF>(a, stream, num_sms);
+}
+
+// Many rows of more than 4 TPR and at most 8 TPR vectors.
+template <int TPR, bool YB, bool HF>
+cudaError_t run_many(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
+  if constexpr (HF) {
+    if (a.nv > 5 * TPR) return run_narrow<2 * TPR, YB, HF>(a, stream, num_sms);
+    return run<TPR, 5, YB, HF>(a, stream, num_sms);
+  } else {
+    return run_wide<TPR, YB, HF>(a, stream, num_sms);
+  }
+}
+
 template <bool YB, bool HF>
 cudaError_t dispatch(const BlockNormArgs& a, cudaStream_t stream, int num_sms) {
-  const bool many = a.T > 4 * num_sms;
+  const bool many = a.T > 4 * num_sms, very_many = a.T > 160 * num_sms;
   if (a.nv <= 64) {
-    if (a.T > 160 * num_sms) return run<8, 8, YB, HF>(a, stream, num_sms);
-    return run<32, 2, YB, HF>(a, stream, num_sms);
+    if (!very_many) return run<32, 2, YB, HF>(a, stream, num_sms);
+    if (a.nv <= 32) return run<8, 4, YB, HF>(a, stream, num_sms);
+    return run_many<8, YB, HF>(a, stream, num_sms);
   }
-  if (a.nv <= 128)
-    return many ? run<32, 4, YB, HF>(a, stream, num_sms) : run<64, 2, YB, HF>(a, stream, num_sms);
-  if (a.nv <= 256 && a.T > num_sms) {
-    if (!many) return run<128, 2, YB, HF>(a, stream, num_sms);
-    if constexpr (HF)
-      return run<64, 4, YB, HF>(a, stream, num_sms);
-    else
-      return run<32, 8, YB, HF>(a, stream, num_sms);
+  if (a.nv <= 128) {
+    if (!many) return run<64, 2, YB, HF>(a, stream, num_sms);
+    if (very_many && a.nv <= 112) return run_many<16, YB, HF>(a, stream, num_sms);
+    return run_narrow<32, YB, HF>(a, stream, num_sms);
   }
-  if (a.nv <= 512) {
-    if (!many) return run<256, 2, YB, HF>(a, stream, num_sms);
-    if constexpr (HF)
-      return run<128, 4, YB, HF>(a, stream, num_sms);
-    else
-      return run<64, 8, YB, HF>(a, stream, num_sms);
-  }
-  if (a.nv <= 1024) {
-    if constexpr (!HF) {
-      if (many) return run<128, 8, YB, HF>(a, stream, num_sms);
-    }
-    return run<256, 4, YB, HF>(a, stream, num_sms);
-  }
+  if (a.nv <= 256 && a.T > num_sms)
+    return many ? run_many<32, YB, HF>(a, stream, num_sms) : run<128, 2, YB, HF>(a, stream, num_sms);
+  if (a.nv <= 512)
+    return many ? run_many<64, YB, HF>(a, stream, num_sms) : run<256, 2, YB, HF>(a, stream, num_sms);
+  if (a.nv <= 1024)
+    return many ? run_many<128, YB, HF>(a, stream, num_sms) : run_narrow<256, YB, HF>(a, stream, num_sms);
   if (a.nv <= 2048)
-    return a.T > num_sms ? run<256, 8, YB, HF>(a, stream, num_sms) : run<512, 4, YB, HF>(a, stream, num_sms);
-  return run<512, 8, YB, HF>(a, stream, num_sms);
+    return a.T > num_sms ? run_wide<256, YB, HF>(a, stream, num_sms) : run<512, 4, YB, HF>(a, stream, num_sms);
+  return run_wide<512, YB, HF>(a, stream, num_sms);
 }
 
 }  // namespace

@@ -59,12 +59,12 @@ cudaError_t block_norm_bwd_post(BwdArgs& a, const GradOut& g, bool y_bf16, bool 
 cudaError_t block_norm_bwd_post_gate(BwdArgs& a, const GradOut& g, bool y_bf16, bool h_f32, int& blocks,
                                      cudaStream_t stream, int num_sms);
 
-// Row lanes of the whole grid at most, over the shapes that a width can take.
+// Row lanes of the whole grid at most, over the shapes that a width can take (12 columns per thread and
+// the fewest threads).
 inline int max_units(int d, int sms) {
-  if (d <= 256) return 16 * sms;
-  if (d <= 512) return 8 * sms;
-  if (d <= 1024) return 4 * sms;
-  if (d <= 2048) return 2 * sms;
+  if (d <= 3 * 128) return 16 * sms;
+  if (d <= 3 * 256) return 8 * sms;
+  if (d <= 3 * 512) return 4 * sms;
   if (d <= 4096) return 2 * sms;
   return sms;
 }
@@ -74,7 +74,7 @@ namespace {
 // Blocks of 256 threads, two per SM, or of the 512 that share one row, one per SM.
 constexpr int bb_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
 constexpr int bb_blocks_per_sm(int tpr) { return tpr > 256 ? 1 : 2; }
-constexpr int bb_ring_bytes(int tpr) { return tpr > 256 ? 216 * 1024 : 104 * 1024; }
+constexpr int bb_ring_bytes(int tpr) { return tpr > 256 ? 224 * 1024 : 108 * 1024; }
 
 template <int TPR, int VPT, int CS, bool YB, bool HF, bool POST, bool GATE>
 __global__ void __launch_bounds__(bb_threads(TPR), bb_blocks_per_sm(TPR)) block_norm_bwd_kernel(const BwdArgs a) {
@@ -440,7 +440,7 @@ template <int TPR, int VPT, int CS, bool YB, bool HF, bool POST, bool GATE>
 cudaError_t run_typed(BwdArgs& a, const GradOut& g, int& blocks, cudaStream_t stream, int num_sms) {
   constexpr int THREADS = bb_threads(TPR), RPB = THREADS / TPR, RING = bb_ring_bytes(TPR);
   auto kern = block_norm_bwd_kernel<TPR, VPT, CS, YB, HF, POST, GATE>;
-  const int smem_max = RING + 64;
+  const int smem_max = RING + 128;  // the barriers of two rows of 8 lanes behind the ring
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
   if (e != cudaSuccess) return e;
   int clusters = bb_blocks_per_sm(TPR) * num_sms / CS;
@@ -455,7 +455,7 @@ cudaError_t run_typed(BwdArgs& a, const GradOut& g, int& blocks, cudaStream_t st
   // a multiple of 16 columns, so that every block's slice of a row starts and ends on 16 bytes
   a.vecs_per_cta = CS > 1 ? (a.nv / 4 + CS - 1) / CS * 4 : a.nv;
   a.slot_bytes = a.vecs_per_cta * a.col_bytes * 4;
-  a.depth = std::max(1, std::min(kBbMaxDepth, (RING + 64) / (RPB * (a.slot_bytes + 8))));
+  a.depth = std::max(1, std::min(kBbMaxDepth, (RING + 128) / (RPB * (a.slot_bytes + 8))));
   const int smem = std::max(RPB * a.depth * (a.slot_bytes + 8), THREADS * VPT * 16 /* the column sums at the end */);
   // where the partial rows go
   const size_t rows = static_cast<size_t>(max_units(a.nv * 4, kBbMaxSms));
@@ -479,24 +479,40 @@ cudaError_t run(BwdArgs& a, const GradOut& g, bool yb, bool hf, int& blocks, cud
             : run_typed<TPR, VPT, CS, false, false, POST, GATE>(a, g, blocks, stream, num_sms);
 }
 
-// 16 columns per thread where two rows can be staged for every row lane, else 8; below 2049 columns 8 is
-// faster either way (16384 x 2048, bf16, one reader: 98 us against 115).
+// Whether two rows can be staged for every row lane of TPR threads.
+inline bool stages_two(const BwdArgs& a, int tpr) {
+  return 2 * (bb_threads(tpr) / tpr) * a.nv * 4 * a.col_bytes <= bb_ring_bytes(tpr);
+}
+
+// Threads per row and vectors per thread: columns that a row does not fill cost what full ones cost, so
+// 12 columns per thread where they hold a row that 8 do not, and 16 beyond 2048 columns, as long as two
+// rows can be staged.  Measured against 8 (16 beyond 2048) alone, 67 MB of y: bf16, one reader: 272 columns
+// 106 us against 150, 528 107 against 154, 1040 112 against 139, 5120 85 against 94; y fp32, a gate row per
+// token, two readers: 528 columns 167 against 235, 2064 145 against 223, 5120 133 against 240 (a cluster).
+// With a row per SM or less 12 columns lose: 126 x 1040 6.0 us against 5.5.  16 columns below 2049: 16384 x
+// 2048, bf16, one reader 115 us against 98.  Clusters of blocks of 256 threads, two per SM, in place of
+// 512: 8192 columns 240 us against 172.
 template <bool POST, bool GATE>
 cudaError_t run_mode(BwdArgs& a, const GradOut& g, bool yb, bool hf, int& blocks, cudaStream_t stream, int num_sms) {
-  const bool wide = a.col_bytes <= 13;
-  const int d = a.nv * 4;
-  if (d <= 256) return run<32, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  if (d <= 512) return run<64, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  if (d <= 1024) return run<128, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  if (d <= 2048) return run<256, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  if (d <= 4096)
-    return wide ? run<256, 4, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
-                : run<512, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  if (d <= 8192)
-    return wide ? run<512, 4, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
-                : run<512, 2, 2, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
-  return wide ? run<512, 4, 2, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
-              : run<512, 2, 4, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  const int nv = a.nv;
+  const auto by_12 = [&](int tpr) { return nv <= 3 * tpr && a.T > num_sms && stages_two(a, tpr); };
+  if (nv <= 64) return run<32, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (by_12(32)) return run<32, 3, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 128) return run<64, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (by_12(64)) return run<64, 3, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 256) return run<128, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (by_12(128)) return run<128, 3, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 512) return run<256, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 768 && stages_two(a, 256)) return run<256, 3, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 1024)
+    return stages_two(a, 256) ? run<256, 4, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
+                              : run<512, 2, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 1536 && stages_two(a, 512)) return run<512, 3, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  if (nv <= 2048)
+    return stages_two(a, 512) ? run<512, 4, 1, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
+                              : run<512, 2, 2, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
+  return a.col_bytes <= 13 ? run<512, 4, 2, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms)
+                           : run<512, 2, 4, POST, GATE>(a, g, yb, hf, blocks, stream, num_sms);
 }
 
 }  // namespace

@@ -353,3 +353,39 @@ def test_gradient_against_differences_of_the_library_s_forward(lib):
         # dY is rounded to bf16 (2^-8 of each term); fp32 noise of h' over the step, and the step's
         # third-order term (step^2 of the terms), stay below the same again
         assert abs(diff - want) <= 2 * UB * size
+
+
+# At and past the widths where a thread gets another vector of 4 columns; K = 64 still covers 16 columns
+# of a thread (16 + 5 + 8 + 6 + 12 + 8 = 55).
+VECTORS = [320, 336, 384, 400, 640, 656, 768, 784, 896, 912, 1280, 1296, 1536, 1552, 1792, 1808, 2560, 2576, 3056, 3088,
+           3584, 3600, 5120, 5136, 6144, 6160, 7168, 7184, 10240, 10256, 12288, 12304, 14336, 14352]
+
+
+@pytest.mark.parametrize("h_f32", [False, True])
+@pytest.mark.parametrize("d", VECTORS)
+def test_widths_between_the_powers_of_two(lib, d, h_f32):
+    k = VECTORS.index(d)
+    T = 601 if d <= 4096 else 151
+    c = Case(T, d, y_bf16=k % 4 < 2, h_f32=h_f32, post=k % 5 != 4, period=[None, 1, 200][k % 3], readers=1 + k // 2 % 3,
+             seed=d)
+    c.buffers()
+    c.forward(lib)
+    lib.sbl_check()
+    c.check_forward()
+    c.backward(lib)
+    lib.sbl_check()
+    c.check_backward()
+
+
+@pytest.mark.parametrize("h_f32", [False, True])
+@pytest.mark.parametrize("d", [112, 128, 144, 160, 176, 192, 208, 240, 272, 336, 400, 464])
+def test_narrow_rows_in_great_number(lib, d, h_f32):
+    k = d // 16
+    c = Case(23711, d, y_bf16=k % 2 == 0, h_f32=h_f32, period=[None, 1, 5000][k % 3], readers=1 + k % 2, seed=d)
+    c.buffers()
+    c.forward(lib)
+    lib.sbl_check()
+    c.check_forward()
+    c.backward(lib)
+    lib.sbl_check()
+    c.check_backward()
