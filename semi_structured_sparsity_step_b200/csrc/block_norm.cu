@@ -138,6 +138,9 @@ __global__ void __launch_bounds__(bn_threads(TPR), bn_blocks(TPR, VPT)) block_no
   if (tr == 0)
     for (int i = 0; i < a.depth; ++i)
       if (row0 + i * stride < a.T) request(row0 + i * stride, i);
+  // With one row per lane the next kernel is set up meanwhile: 1 x 2048 and the 8-bit product 2048 -> 11008
+  // that reads it 7.8 us, without 9.6.  A grid that stays loses: 4096 x 2048 18.4 us against 17.6.
+  if (a.T <= stride) pdl::release();
 
   RingPos pos;
   for (long long base = static_cast<long long>(blockIdx.x) * RPB; base < a.T; base += stride) {

@@ -122,10 +122,7 @@ __global__ void __launch_bounds__(kW8Threads) w8a8_stream_kernel(const __grid_co
   if (warp == 0) {
     if (lane == 0) {
       pdl::wait();
-      // The successor may be set up from here on: this block has its tensor memory, and what the kernels
-      // before this one wrote is visible, so a successor that reads ahead of its own wait (the decode
-      // GEMVs read packed weights) reads it whole.
-      asm volatile("griddepcontrol.launch_dependents;");
+      pdl::release();  // this block has its tensor memory
       int it = 0;
       bool ok = true;
       for (int kb = kb0; kb < kb1; ++kb, ++it) {

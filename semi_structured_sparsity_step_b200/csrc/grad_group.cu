@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kGgThreads) grad_sumsq_kernel(const __grid_con
                                                                 double* __restrict__ partial, unsigned keep) {
   __shared__ double scratch[kGgThreads / 32];
   pdl::wait();
-  asm volatile("griddepcontrol.launch_dependents;");
+  pdl::release();
   const unsigned total = tab.tile_start[tab.count];
   const uint64_t normal = policy_normal(), first = policy_first();
   double s = 0.0;

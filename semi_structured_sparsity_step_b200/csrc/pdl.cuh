@@ -12,6 +12,11 @@ namespace pdl {
 
 __device__ __forceinline__ void wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The next kernel may be set up once every block has called this or ended.  Called behind wait(), so that
+// a kernel that reads ahead of its own wait (the decode GEMVs read packed weights) finds whole what
+// the kernels before this one wrote.
+__device__ __forceinline__ void release() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kern)(KArgs...), int grid, int threads, int smem, int cluster, cudaStream_t stream,
                    Args&&... args) {
