@@ -295,7 +295,7 @@ cudaError_t run(BlockNormArgs a, cudaStream_t stream, int num_sms) {
 //     37 against 78; 272 columns, 15420 rows 16.8 against 15.8, 61680 rows 41.8 against 50.6;
 //     512 columns, 65536 rows 66.5 with 16 of 8 against 64.0 with 32 of 4;
 //   896 columns: 1 row 2.4 us with 256 threads, 2.6 with 128; 1000 rows 4.4 with 128, 5.9 with 4 vectors
-//     each; 16000 rows 31.5 with 32 of 7, 35.1 with 64 of 4;
+//     each; 16000 rows 31.5 with 32 of 8 (7 fill it), 35.1 with 64 of 4;
 //   2048 columns: 300 rows 3.7 us with 256 threads, 4.5 with 64 of 8; 16000 rows 60.3 with 64 of 8,
 //     68.5 with 128 of 4;
 //   4096 columns: 300 rows 4.7 us with 256 of 4, 5.6 with 128 of 8; 16000 rows 126 against 117;
