@@ -176,40 +176,66 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& a, float* tile, i
   __syncwarp();
 }
 
-// The same for the 8-bit product: scale (the token's) and sw (the chunk's 32 columns', in shared
-// memory) both in the row layout, so a bf16 chunk is packed before it is turned around and passes
-// shared memory at half the size, 16 bytes per lane and access.
+// Barrier 1 of N threads, which tells all of them whether any has x set.
+template <int N>
+__device__ __forceinline__ bool bar_any(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(x ? 1u : 0u), "n"(N)
+      : "memory");
+  return any != 0u;
+}
+
+// The same for the 8-bit product: scale (the token's) and sw (the columns', in shared memory) both in
+// the row layout.  A bf16 chunk is packed before it is turned around, and two of them are, so that a row's
+// segment is 128 bytes in either type.
+__device__ __forceinline__ void scaled_w8_bf16(uint32_t* t, const uint32_t (&r)[32], float scale, const float* sw) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 s = *reinterpret_cast<const float2*>(sw + j + 2 * k);
+      const __nv_bfloat162 p =
+          __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k])), scale), s.x),
+                                __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k + 1])), scale), s.y));
+      w[k] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    *reinterpret_cast<uint4*>(t + j / 2) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Columns [col0, col0 + 32), of bf16 [col0, col0 + 64), of a warp's 32 rows; `at` is their place in
+// tensor memory.
 template <bool kBf16>
 __device__ __forceinline__ void epilogue_chunk_w8(const GemmArgs& a, float* tile, int row0, int col0, int lane,
-                                                  const uint32_t (&r)[32], float scale, const float* sw) {
+                                                  uint32_t at, float scale, const float* sw) {
+  constexpr int LD = 36;  // words per row: 16-byte accesses of 8 rows hit every bank once
   if constexpr (kBf16) {
-    constexpr int LD = 20;  // words per row of 16 (32 columns): 16-byte accesses of 8 rows hit every bank once
+    uint32_t r0[32], r1[32];
+    tmem_ld_32x32b_x32(at, r0);
+    tmem_ld_32x32b_x32(at + 32, r1);
+    tmem_ld_wait_for(r0);
+    tmem_ld_wait_for(r1);
     uint32_t* t = reinterpret_cast<uint32_t*>(tile);
-#pragma unroll
-    for (int j = 0; j < 32; j += 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 s = *reinterpret_cast<const float2*>(sw + j + 2 * k);
-        const __nv_bfloat162 p =
-            __floats2bfloat162_rn(__fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k])), scale), s.x),
-                                  __fmul_rn(__fmul_rn(__int2float_rn(static_cast<int>(r[j + 2 * k + 1])), scale), s.y));
-        w[k] = *reinterpret_cast<const uint32_t*>(&p);
-      }
-      *reinterpret_cast<uint4*>(t + lane * LD + j / 2) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    scaled_w8_bf16(t + lane * LD, r0, scale, sw);
+    scaled_w8_bf16(t + lane * LD + 16, r1, scale, sw + 32);
     __syncwarp();
-    const int cq = (lane & 3) * 8;
+    const int cq = (lane & 7) * 8;
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int rr = it * 8 + (lane >> 2);
+    for (int it = 0; it < 8; ++it) {
+      const int rr = it * 4 + (lane >> 3);
       if (row0 + rr < a.M && col0 + cq < a.N)  // N % 8 == 0
         __stcs(reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) +
                                         static_cast<long long>(row0 + rr) * a.ldo + col0 + cq),
                *reinterpret_cast<const uint4*>(t + rr * LD + cq / 2));
     }
   } else {
-    constexpr int LD = 36;  // 16-byte accesses of 8 rows hit every bank once
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(at, r);
+    tmem_ld_wait_for(r);
 #pragma unroll
     for (int j = 0; j < 32; j += 4) {
       const float4 s = *reinterpret_cast<const float4*>(sw + j);
@@ -412,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 //             both producers' TMA loads complete on it.
 //   empty[s]  (both CTAs): freed by one multicast tcgen05.commit.
 //   tfull[b]  (both CTAs): accumulator buffer b ready (multicast commit).
-//   tempty[b] (even CTA only): 4 epilogue warps of each CTA arrive.
-template <bool kI8, bool kAMN, bool kBMN, int STAGES, int KP = 0>
+//   tempty[b] (even CTA only): the epilogue warps of each CTA arrive (4, 8 in the 8-bit product).
+template <bool kI8, bool kAMN, bool kBMN, int STAGES, int KP = 0, int EPI = kEpiFwd>
 struct Cfg2 {
   static constexpr int BN = 256;                 // N of the pair's tile
   static constexpr int BK = kI8 ? 128 : 64;      // elements per stage along K (128 bytes)
@@ -421,13 +447,14 @@ struct Cfg2 {
   static constexpr int A_BYTES = 128 * 128;      // this CTA's 128 A rows
   static constexpr int B_BYTES = 128 * 128;      // this CTA's 128 B rows
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int EPI_WARPS = epi_w8(EPI) ? 8 : 4;
   static constexpr int EPI_WARP_FLOATS = 32 * 36;  // rows of 33 words, or 36 (the 8-bit product)
-  static constexpr int EPI_BYTES = 4 * EPI_WARP_FLOATS * 4;
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_WARP_FLOATS * 4;
   // Packed B (KP > 0): per-lane replicated decode tables after the barriers.
   static constexpr int LUT_BYTES = KP > 0 ? 256 * 32 * 8 + 256 * 8 : 0;
   static constexpr int SCALE_BYTES = 2 * BN * 4;  // 8-bit product: the column scales of two tiles
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 1024 + 256 + LUT_BYTES + SCALE_BYTES;
-  static constexpr int THREADS = KP > 0 ? 448 : 192;  // packed: + 8 decoder warps
+  static constexpr int THREADS = KP > 0 ? 448 : 64 + 32 * EPI_WARPS;  // packed: + 8 decoder warps
   static constexpr uint32_t TMEM_COLS = 2 * BN;
   static constexpr uint32_t IDESC = instr_desc(kI8, 256, BN, kAMN, kBMN);
 };
@@ -531,10 +558,10 @@ struct alignas(64) PairGroup {
 };
 
 template <bool kI8, bool kAMN, bool kBMN, int STAGES, int EPI, int KP = 0, int G = 1>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<kI8, kAMN, kBMN, STAGES, KP, EPI>::THREADS, 1)
     tc_gemm_pair_kernel(const __grid_constant__ PairGroup<G> grp, const PackedB pb) {
   const GemmArgs& args = grp.args[0];  // fields shared by the group (err) and the single product
-  using C = Cfg2<kI8, kAMN, kBMN, STAGES, KP>;
+  using C = Cfg2<kI8, kAMN, kBMN, STAGES, KP, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* epi_tiles = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES);
@@ -575,7 +602,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 8);
+      mbar_init(&tempty[b], 2 * C::EPI_WARPS);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -757,19 +784,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
     }
   } else {
     const int q = warp & 3;
-    float* tile = epi_tiles + q * C::EPI_WARP_FLOATS;
-    // 8-bit product: each of the 128 epilogue threads holds two column maxima of the tile to come
+    float* tile = epi_tiles + (warp - 2) * C::EPI_WARP_FLOATS;
+    // 8-bit product: each of the 256 epilogue threads holds a column maximum of the tile to come
     const int et = (warp - 2) * 32 + lane;
-    float wmax_next[2] = {0.0f, 0.0f};
+    float wmax_next = 0.0f;
+    bool failed = false;
     auto fetch_wmax = [&](int w) {
       if (w >= grp.total) return;
       int pi, mb, nb, sp;
       grp.locate(w, pi, mb, nb, sp);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int c = nb * C::BN + et + 128 * k;
-        wmax_next[k] = c < grp.args[pi].N ? __ldg(grp.args[pi].wmax + c) : 0.0f;
-      }
+      const int c = nb * C::BN + et;
+      wmax_next = c < grp.args[pi].N ? __ldg(grp.args[pi].wmax + c) : 0.0f;
     };
     if constexpr (epi_w8(EPI)) fetch_wmax(pair_id);
     int t = 0;
@@ -781,17 +806,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
       if constexpr (epi_w8(EPI)) {
         // this tile's column scales, requested a tile ago; two buffers, as a warp may still be in the
         // tile before
-#pragma unroll
-        for (int k = 0; k < 2; ++k) col_scale[b * C::BN + et + 128 * k] = __fdiv_rn(wmax_next[k], 127.0f);
+        col_scale[b * C::BN + et] = __fdiv_rn(wmax_next, 127.0f);
         fetch_wmax(w + n_pairs);
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-      }
-      if (!mbar_wait(&tfull[b], static_cast<uint32_t>(t >> 1) & 1u, abort_flag, args.err)) {
+        if (bar_any<32 * C::EPI_WARPS>(failed)) break;
+        // a warp whose wait ran out leaves at the next tile's barrier, with all the others
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&tfull[b], static_cast<uint32_t>(t >> 1) & 1u, abort_flag, args.err))) {
+          give_up();
+          failed = true;
+          continue;
+        }
+      } else if (!mbar_wait(&tfull[b], static_cast<uint32_t>(t >> 1) & 1u, abort_flag, args.err)) {
         give_up();
         break;
       }
       tc_fence_after();
-      if (*abort_flag) break;
+      if constexpr (!epi_w8(EPI)) {
+        if (*abort_flag) break;
+      }
       const int row0 = mb * 256 + 128 * static_cast<int>(rank) + 32 * q;
       const int row = row0 + lane;
       float scale = 0.0f;
@@ -803,17 +834,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(KP > 0 ? 448 : kThre
         scale = *A.gamma;
       }
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * C::BN);
+      if constexpr (epi_w8(EPI)) {
+        // two warps share a lane quarter, each has half of the columns
+        constexpr int STEP = EPI == kEpiW8Bf16 ? 64 : 32;
+        const int c_lo = (warp - 2) / 4 * (C::BN / 2);
 #pragma unroll 1
-      for (int c = 0; c < C::BN / 32; ++c) {
-        const int col0 = nb * C::BN + 32 * c;
-        if (col0 >= A.N) break;  // warp-uniform
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(32 * c), r);
-        tmem_ld_wait();
-        if constexpr (epi_w8(EPI))
-          epilogue_chunk_w8<EPI == kEpiW8Bf16>(A, tile, row0, col0, lane, r, scale, col_scale + b * C::BN + 32 * c);
-        else
+        for (int c = c_lo; c < c_lo + C::BN / 2; c += STEP) {
+          const int col0 = nb * C::BN + c;
+          if (col0 >= A.N) break;  // warp-uniform
+          epilogue_chunk_w8<EPI == kEpiW8Bf16>(A, tile, row0, col0, lane, tbase + static_cast<uint32_t>(c), scale,
+                                               col_scale + b * C::BN + c);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < C::BN / 32; ++c) {
+          const int col0 = nb * C::BN + 32 * c;
+          if (col0 >= A.N) break;  // warp-uniform
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(tbase + static_cast<uint32_t>(32 * c), r);
+          tmem_ld_wait();
           epilogue_chunk<EPI>(A, tile, row0, col0, lane, r, scale);
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -956,7 +997,7 @@ int pick_strip(int Mt, int Nt, int c, double a_bytes, double b_bytes) {
 template <bool kI8, bool kAMN, bool kBMN, int STAGES, int EPI, int KP = 0>
 cudaError_t run_pair(const CUtensorMap& ta, const CUtensorMap& tb, const GemmArgs& a, int splits, int num_sms,
                      cudaStream_t stream, double a_bytes, double b_bytes, const PackedB& pb = PackedB{}) {
-  using C = Cfg2<kI8, kAMN, kBMN, STAGES, KP>;
+  using C = Cfg2<kI8, kAMN, kBMN, STAGES, KP, EPI>;
   auto kern = tc_gemm_pair_kernel<kI8, kAMN, kBMN, STAGES, EPI, KP, 1>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -1101,8 +1142,8 @@ cudaError_t launch_forward_w8a8_pair(const int8_t* Xq, const float* amax, const 
   a.wmax = wmax;
   a.err = err;
   const double ab = static_cast<double>(T) * d_in, bb = static_cast<double>(d_out) * d_in;
-  return y_bf16 ? run_pair<true, false, false, kPairStages, kEpiW8Bf16>(ta, tb, a, 1, num_sms, stream, ab, bb)
-                : run_pair<true, false, false, kPairStages, kEpiW8F32>(ta, tb, a, 1, num_sms, stream, ab, bb);
+  return y_bf16 ? run_pair<true, false, false, kPairStages - 1, kEpiW8Bf16>(ta, tb, a, 1, num_sms, stream, ab, bb)
+                : run_pair<true, false, false, kPairStages - 1, kEpiW8F32>(ta, tb, a, 1, num_sms, stream, ab, bb);
 }
 
 cudaError_t launch_forward_group(const FwdProblemDev* probs, int count, cudaStream_t stream, int num_sms,
@@ -1124,7 +1165,7 @@ cudaError_t launch_forward_group(const FwdProblemDev* probs, int count, cudaStre
     }
     return cudaSuccess;
   }
-  using C = Cfg2<true, false, false, kPairStages, 0>;
+  using C = Cfg2<true, false, false, kPairStages>;
   for (int c0 = 0; c0 < count; c0 += kFwdGroup) {
     const int cnt = (count - c0) < kFwdGroup ? (count - c0) : kFwdGroup;
     // longest K first: those items take longest and should start first
