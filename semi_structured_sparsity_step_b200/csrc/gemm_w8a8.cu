@@ -25,6 +25,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <cmath>
 #include <cstdint>
 
 #include "pdl.cuh"
@@ -277,29 +278,31 @@ struct W8Plan {
   int bn, cs;
 };
 
-// The fastest by a model of the time in ns, fitted to 43 shapes (T 1 .. 8192, d_in 128 .. 11008, d_out
-// 128 .. 32768), on which the plan it picks is within 6% of the fastest of all token tiles and splits
-// but for three (10, 13 and 16%):
-//   streaming kernel: 3200 for the launch, plus the longer of
-//     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 160 bytes/ns, or 110
-//     with one ring of about 100 KB in flight, and
-//     Wq from HBM at 6500 bytes/ns or 50 per block of the last wave, a quarter more for each further
-//     token tile,
-//   plus the end of a block, once per wave: 600 + 24 per token column, or 1500 + 26 with a cluster's
-//   exchange (and then one wave at most);
-//   CTA-pair kernel: 6200, plus the longer of both operands from HBM at 4500 bytes/ns and, for each wave
-//   of 256 x 256 tiles, the longer of 263 per K block and the 3900 of a tile's epilogue.
+// The fastest by a model of the time in ns, fitted to 458 cases (T 1 .. 8192, d_in 128 .. 11008, d_out
+// 128 .. 32768, both types), on which the plan it picks is 1.1% above the fastest of all token tiles and
+// splits on average, and more than 10% above it in 14 cases (the worst 19%):
+//   streaming kernel: 4000 for the launch, plus the longest of
+//     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 186 bytes/ns, 89 with
+//     more than one block on it, 168 at BN 256,
+//     what all copy together at 18200 bytes/ns, and
+//     Wq from HBM at 5500 bytes/ns or 54 per block of the last wave, half more for each further token tile,
+//   plus the end of a block, once per wave: 540 + 21.3 per token column (14.1 of fp32), or 1230 + 19.3
+//   with a cluster's exchange (and then one wave at most);
+//   CTA-pair kernel: 7700, plus the longer of both operands from HBM at 4800 bytes/ns and, for each wave
+//   of 256 x 256 tiles, the longer of 205 per K block and the 1550 (fp32 3200) of a tile's epilogue.
+// The constants are those of the best fit, where a choice depends on differences, not rates of the machine.
 // Measured, best plan against one fixed choice (token tile >= T, as many splits as fit):
 // 512 x 2048 x 2048 7.6 us against 12.4, 256 x 2048 x 2048 7.5 against 19.9, 1 x 2048 x 32768 13.7
 // against 22.5 on CTA pairs, 2048 x 896 x 4864 17.0 on CTA pairs against 20.5.
-W8Plan plan_w8a8(int T, int d_in, int d_out, int num_sms) {
+W8Plan plan_w8a8(int T, int d_in, int d_out, bool y_bf16, int num_sms) {
   const double KB = (d_in + 127) / 128, mt = (d_out + kW8Rows - 1) / kW8Rows;
   const double pair_tiles = static_cast<double>((T + 255) / 256) * ((d_out + 255) / 256);
   const double pairs = num_sms / 2;
-  const double pair_wave = KB * 263.0 > 3900.0 ? KB * 263.0 : 3900.0;
+  const double pair_end = y_bf16 ? 1550.0 : 3200.0;
+  const double pair_wave = KB * 205.0 > pair_end ? KB * 205.0 : pair_end;
   const double pair_math = static_cast<double>(static_cast<long long>((pair_tiles + pairs - 1) / pairs)) * pair_wave;
-  const double pair_hbm = (static_cast<double>(d_out) + T) * d_in / 4500.0;
-  double best = 6200.0 + (pair_math > pair_hbm ? pair_math : pair_hbm);
+  const double pair_hbm = (static_cast<double>(d_out) + T) * d_in / 4800.0;
+  double best = 7700.0 + (pair_math > pair_hbm ? pair_math : pair_hbm);
   W8Plan plan{0, 1};
   for (int bn = 16; bn <= 256; bn *= 2) {
     const double nt = (T + bn - 1) / bn;
@@ -307,16 +310,19 @@ W8Plan plan_w8a8(int T, int d_in, int d_out, int num_sms) {
       const double blocks = mt * nt * cs;
       const double per_sm = static_cast<double>(static_cast<long long>((blocks + num_sms - 1) / num_sms));
       const double kb = static_cast<double>(static_cast<long long>((KB + cs - 1) / cs));
-      const double copy = per_sm * kb * (16384.0 + 128.0 * bn) / (per_sm > 1 || bn == 256 ? 160.0 : 110.0);
-      // clusters do not pack every SM: 264 of 296 places are counted on (288 were measured to take two waves)
-      const double resident = num_sms * (bn == 256 ? 1.0 : 2.0) * (cs == 1 ? 1.0 : bn == 256 ? 0.95 : 0.9);
-      const double waves = static_cast<double>(static_cast<long long>((blocks + resident - 1) / resident));
+      const double block_bytes = kb * (16384.0 + 128.0 * bn);
+      const double copy = per_sm * block_bytes / (bn == 256 ? 168.0 : per_sm > 1 ? 89.0 : 186.0);
+      const double copy_all = blocks * block_bytes / 18200.0;
+      // clusters do not pack every SM: 254 of 296 places are counted on (288 were measured to take two waves)
+      const double resident = num_sms * (bn == 256 ? 1.0 : 2.0) * (cs == 1 ? 1.0 : bn == 256 ? 0.97 : 0.86);
+      const double waves = std::ceil(blocks / resident);
       const double last = (blocks - (waves - 1) * resident) / blocks;  // the last wave's share of the blocks
-      const double wq = static_cast<double>(d_out) * d_in * (1.0 + 0.25 * (nt - 1));
-      const double last_rate = last * blocks * 50.0 < 6500.0 ? last * blocks * 50.0 : 6500.0;
-      const double hbm = wq * (1.0 - last) / 6500.0 + wq * last / last_rate;
-      const double t =
-          3200.0 + (copy > hbm ? copy : hbm) + waves * (cs > 1 ? 1500.0 + 26.0 * bn : 600.0 + 24.0 * bn);
+      const double wq = static_cast<double>(d_out) * d_in * (1.0 + 0.5 * (nt - 1));
+      const double last_rate = last * blocks * 54.0 < 5500.0 ? last * blocks * 54.0 : 5500.0;
+      const double hbm = wq * (1.0 - last) / 5500.0 + wq * last / last_rate;
+      const double move = copy > copy_all ? copy : copy_all;
+      const double t = 4000.0 + (move > hbm ? move : hbm) +
+                       waves * (cs > 1 ? 1230.0 + 19.3 * bn : 540.0 + (y_bf16 ? 21.3 : 14.1) * bn);
       if ((cs == 1 || waves == 1) && t < best) {
         best = t;
         plan = W8Plan{bn, cs};
@@ -343,7 +349,7 @@ cudaError_t dispatch(const int8_t* Xq, const int8_t* Wq, int d_in, const W8Args&
 
 cudaError_t launch_w8a8(const int8_t* Xq, const float* amax, const int8_t* Wq, const float* wmax, int T, int d_in,
                         int d_out, bool y_bf16, void* Y, cudaStream_t stream, int num_sms, uint32_t* err) {
-  const W8Plan p = plan_w8a8(T, d_in, d_out, num_sms);
+  const W8Plan p = plan_w8a8(T, d_in, d_out, y_bf16, num_sms);
   if (p.bn == 0)
     return launch_forward_w8a8_pair(Xq, amax, Wq, wmax, T, d_in, d_out, y_bf16, Y, stream, num_sms, err);
   W8Args a{};

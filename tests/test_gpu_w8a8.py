@@ -62,6 +62,21 @@ def test_full_batches(lib, T, d_in, d_out, bf16):
     _run(lib, T, d_in, d_out, bf16, seed=T, sample=200)
 
 
+# Token tile and K splits that the plan takes there: 32 (1 to 8 splits), 64, 128, 256 (1 to 5), CTA pairs.
+STREAMED = [(1451, 16, 160, 0), (168, 16, 3416, 1), (17, 2016, 6816, 0), (958, 2288, 24, 0), (771, 2112, 32, 1),
+            (551, 3120, 16, 1), (552, 2720, 16, 0), (476, 2640, 16, 1), (437, 3616, 16, 0), (260, 16, 4520, 0),
+            (70, 2064, 3456, 1), (1913, 4128, 16, 0), (1722, 4896, 16, 1), (1462, 4816, 16, 0), (1282, 4496, 16, 1),
+            (1102, 7760, 16, 1), (943, 5856, 16, 0), (500, 16, 4848, 0), (325, 16, 7040, 1), (143, 3424, 3184, 0),
+            (66, 3152, 4424, 1), (65, 4112, 3552, 1), (2505, 9248, 24, 0), (2803, 9616, 16, 1), (70, 6976, 2000, 0),
+            (65, 7808, 1776, 1), (462, 528, 4776, 0), (131, 5808, 6376, 1), (131, 4976, 5264, 0), (130, 7056, 3896, 1),
+            (131, 8320, 3176, 0), (265, 1168, 6808, 0), (2634, 16, 2112, 1)]
+
+
+@pytest.mark.parametrize("T,d_in,d_out,bf16", STREAMED)
+def test_every_tile_and_split_of_the_plan(lib, T, d_in, d_out, bf16):
+    _run(lib, T, d_in, d_out, bool(bf16), seed=d_in + T)
+
+
 def test_the_two_kernels_agree(lib):
     """The same tokens in a short and in a full batch."""
     d_in, d_out = 1040, 5000
