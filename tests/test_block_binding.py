@@ -1,0 +1,103 @@
+"""The binding and the layer helpers of the operators around the products, on the CPU: the library call is
+replaced by one that records what would reach it, host tensors stand for device tensors."""
+import ctypes
+
+import pytest
+import torch
+
+from semi_structured_sparsity_step_b200 import _binding as B
+
+BF16, I8 = torch.bfloat16, torch.int8
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = []
+    monkeypatch.setattr(B, "_torch", torch)
+    monkeypatch.setattr(B, "_device", lambda: -1)  # what get_device() gives for a host tensor
+    monkeypatch.setattr(B, "_call", lambda name, *args: got.append((name, args)))
+    return got
+
+
+T, D, D_OUT = 5, 32, 16
+
+
+def _norm(**kw):
+    h = torch.zeros(T, D, dtype=BF16)
+    a = dict(Y=torch.zeros(T, D), H=h, g_post=h[0], gate=h, gate_period=1, res_scale=1.0, g_pre=h[0], eps=1e-6, T=T, d=D,
+             flags=0, H_out=h, Xn=h, Xq=torch.zeros(T, D, dtype=I8), amax=torch.zeros(T), rstd=torch.zeros(2 * T), stream=0)
+    return B.sbl_block_norm(**dict(a, **kw))
+
+
+def _norm_backward(**kw):
+    h, x = torch.zeros(T, D, dtype=BF16), torch.zeros(T, D)
+    a = dict(dXn=[x], dH_out=h, Y=x, H_out=h, g_post=h[0], gate=h, gate_period=1, res_scale=1.0, g_pre=h[0],
+             rstd=torch.zeros(2 * T), T=T, d=D, flags=0, dY=h, dH=h, dg_post=x[0], dg_pre=x[0], dgate=x, accumulate=0,
+             workspace=torch.zeros(64, dtype=torch.uint8), workspace_bytes=64, stream=0)
+    return B.sbl_block_norm_backward(**dict(a, **kw))
+
+
+def _w8a8(**kw):
+    a = dict(Xq=torch.zeros(T, D, dtype=I8), amax=torch.zeros(T), Wq=torch.zeros(D_OUT, D, dtype=I8),
+             wmax=torch.zeros(D_OUT), T=T, d_in=D, d_out=D_OUT, flags=0, Y=torch.zeros(T, D_OUT), stream=0)
+    return B.sbl_forward_w8a8(**dict(a, **kw))
+
+
+def _grads(fn):
+    def call(**kw):
+        g = torch.zeros(64)
+        a = dict(tensors=[(g, g, 64, False)], sumsq=torch.zeros(1, dtype=torch.float64), norm=torch.zeros(1),
+                 workspace=torch.zeros(64, dtype=torch.uint8), workspace_bytes=64, stream=0)
+        if fn is B.sbl_grad_clip_group:
+            a.update(max_norm=1.0, clip=torch.zeros(1))
+        return fn(**dict(a, **kw))
+    return call
+
+
+CALLS = {"norm": _norm, "norm_backward": _norm_backward, "w8a8": _w8a8, "clip": _grads(B.sbl_grad_clip_group),
+         "grad_norm": _grads(B.sbl_grad_norm_group)}
+INT = 2 ** 32  # an int or an unsigned of the library keeps its last 32 bits
+
+
+@pytest.mark.parametrize("which,name,value", [
+    ("norm", "T", T - INT), ("norm", "d", D - INT), ("norm", "flags", -INT), ("norm", "flags", INT),
+    ("norm_backward", "T", T - INT), ("norm_backward", "d", D - INT), ("norm_backward", "flags", INT), ("norm_backward", "flags", -INT), ("norm_backward", "accumulate", INT),
+    ("norm_backward", "accumulate", 1 - INT),
+    ("w8a8", "T", T - INT), ("w8a8", "d_in", D - INT), ("w8a8", "d_out", D_OUT - INT), ("w8a8", "flags", INT),
+    # a size_t keeps the last 64: one byte too few would arrive as more than any workspace needs
+    ("norm_backward", "workspace_bytes", -1), ("norm_backward", "workspace_bytes", 64 - 2 ** 64),
+    ("clip", "workspace_bytes", -1), ("grad_norm", "workspace_bytes", -1),
+    ("clip", "tensors", [(1 << 12, 1 << 12, -1, False)]), ("grad_norm", "tensors", [(1 << 12, None, 2 ** 64, False)]),
+])
+def test_integers_that_the_library_would_cut_are_refused(calls, which, name, value):
+    call = CALLS[which]
+    call()
+    assert len(calls) == 1
+    with pytest.raises(B.SblError):
+        call(**{name: value})
+    assert len(calls) == 1
+
+
+def test_integers_of_the_library_s_width_reach_it(calls):
+    """The library answers for what its own types can hold: both ends of an int arrive as they are."""
+    for T_ in (-1, -2 ** 31):
+        _norm(T=T_)
+        _w8a8(T=T_)
+    assert [ctypes.c_int(c[1][i]).value for c, i in zip(calls, (8, 4, 8, 4))] == [-1, -1, -2 ** 31, -2 ** 31]
+
+
+@pytest.mark.parametrize("period", [0, -1, -2 ** 31, 1 - INT, -2 ** 63])
+def test_a_gate_period_below_one_never_arrives_as_a_period(calls, period):
+    """1 - 2^32 would be cut to 1, one gate row per token, with no row of the gate asked for."""
+    _norm(gate_period=period)
+    _norm_backward(gate_period=period)
+    assert all(ctypes.c_int(c[1][i]).value < 1 for c, i in zip(calls, (4, 7)))
+
+
+@pytest.mark.parametrize("fn", ["sbl_grad_group_workspace_bytes", "sbl_block_norm_backward_workspace_bytes"])
+@pytest.mark.parametrize("value", [2 ** 32 + 16, 16 - 2 ** 32])
+def test_workspace_of_a_size_that_is_no_int_is_none(fn, value):
+    from semi_structured_sparsity_step_b200 import build
+    build.build()
+    assert getattr(B, fn)(16) > 0
+    assert getattr(B, fn)(value) == 0
