@@ -66,19 +66,33 @@ def act_quant(X: torch.Tensor, Xq: torch.Tensor, amax: torch.Tensor, stream=None
     B.sbl_act_quant(X, T, d_in, Xq, amax, stream)
 
 
+def _rows_of(fn, width, *tensors):
+    """Refuses tensors that are not [rows, width].  A call takes a contiguous buffer of at least as many
+    elements as it has tokens: it would read [batch, sequence, width] as its first rows, and halves of
+    wider rows as rows.  A buffer may hold more rows than the call has tokens; they stay as they are."""
+    for x in tensors:
+        if x is not None and x.__class__ is not int and (x.dim() != 2 or x.shape[1] != width):
+            raise B.SblError(fn, 2)
+
+
 class BlockNorm:
     """Norm of a branch output, gate, scaled residual, next norm and int8 codes
     (sbl_block_norm), with its backward, for up to `max_tokens` tokens.
 
     g_pre, g_post: bf16 gains of the norms after and before the sum (g_post
     None: the branch is not normalised).  The outputs and the factors that the
-    backward needs live here and are overwritten by the next call."""
+    backward needs live here and are overwritten by the next call.
+
+    Activations and their gradients are [tokens, d], gates [rows, d], with as
+    many tokens as Y has (a [batch, sequence, d] is flattened by the caller);
+    tensors of other dimensions or widths raise SblError."""
 
     def __init__(self, g_pre: torch.Tensor, g_post: torch.Tensor | None = None, max_tokens: int = 1,
                  res_scale: float = 1.0, eps: float = 1e-6, y_dtype=torch.float32, h_dtype=torch.bfloat16):
         assert g_pre.is_cuda and g_pre.dtype == torch.bfloat16
         assert y_dtype in (torch.float32, torch.bfloat16) and h_dtype in (torch.float32, torch.bfloat16)
         dev, d = g_pre.device, g_pre.numel()
+        assert g_post is None or g_post.numel() == d
         self.g_pre, self.g_post, self.d, self.res_scale, self.eps = g_pre, g_post, d, res_scale, eps
         self.flags = (B.SBL_BLOCK_Y_BF16 if y_dtype == torch.bfloat16 else 0) | \
             (B.SBL_BLOCK_H_F32 if h_dtype == torch.float32 else 0)
@@ -96,6 +110,7 @@ class BlockNorm:
     def forward(self, Y, H, gate=None, gate_period=0, stream=None):
         """-> (H_out, Xn, Xq, amax) of the call's tokens."""
         T = Y.shape[0]
+        _rows_of("sbl_block_norm", self.d, Y, H, gate)
         B.sbl_block_norm(Y, H, self.g_post, gate, gate_period, self.res_scale, self.g_pre, self.eps, T, self.d,
                          self.flags, self.H_out, self.Xn, self.Xq, self.amax, self.rstd, stream)
         self.T = T
@@ -106,6 +121,7 @@ class BlockNorm:
         to dg_pre and dg_post.  The tokens are those of the last forward, whose H_out and factors it
         uses; Y may be None where nothing needs it (no g_post, no dgate)."""
         assert dY.shape[0] == self.T  # the factors lie as that many tokens left them
+        _rows_of("sbl_block_norm_backward", self.d, *dXn, dH_out, Y, dY, dH, gate, dgate)
         if self.ws is None:
             self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
         B.sbl_block_norm_backward(dXn, dH_out, Y, self.H_out, self.g_post, gate, gate_period, self.res_scale,
@@ -117,7 +133,9 @@ class Int8Linear:
     """A projection held in 8 bits: W [d_out, d_in] bf16, quantised row by row.
 
     weight_step() quantises W again after it has changed.  backward() is the
-    straight-through estimator on the bf16 W: dX = dY . W, dW = dY^T . X."""
+    straight-through estimator on the bf16 W: dX = dY . W, dW = dY^T . X.
+    Activations and their gradients are [tokens, d_in] and [tokens, d_out], dW
+    [d_out, d_in] or flat; tensors of other dimensions or widths raise SblError."""
 
     def __init__(self, W: torch.Tensor):
         assert W.is_cuda and W.dtype == torch.bfloat16 and W.is_contiguous()
@@ -135,6 +153,8 @@ class Int8Linear:
 
     def forward(self, Xq, amax, Y, stream=None):
         """Y [T, d_out] in fp32 or bf16, by its type."""
+        _rows_of("sbl_forward_w8a8", self.d_in, Xq)
+        _rows_of("sbl_forward_w8a8", self.d_out, Y)
         flags = B.SBL_W8A8_Y_BF16 if Y.dtype == torch.bfloat16 else 0
         B.sbl_forward_w8a8(Xq, amax, self.Wq, self.wmax, Xq.shape[0], self.d_in, self.d_out, flags, Y, stream)
 
@@ -143,6 +163,8 @@ class Int8Linear:
         T, a = dY.shape[0], B._args("sbl_backward")
         f32, bf16 = torch.float32, torch.bfloat16
         n = self.d_out * self.d_in
+        _rows_of("sbl_backward", self.d_out, dY)
+        _rows_of("sbl_backward", self.d_in, X, dX, dW if dW is None or dW.dim() != 1 else None)
         B.sbl_backward(a(dY, bf16, T * self.d_out), a(X, bf16, T * self.d_in), a(self.W, bf16, n), self.one, T,
                        self.d_in, self.d_out, a(dX, f32, T * self.d_in), a(dW, f32, n), int(accumulate_dW), None, 0,
                        stream)

@@ -101,3 +101,91 @@ def test_workspace_of_a_size_that_is_no_int_is_none(fn, value):
     build.build()
     assert getattr(B, fn)(16) > 0
     assert getattr(B, fn)(value) == 0
+
+
+# ---- layer helpers: [tokens, width] and nothing that would be read as something else
+
+def _block_norm(post=True):
+    from semi_structured_sparsity_step_b200 import layer
+    gain = torch.ones(D, dtype=BF16)
+    N = object.__new__(layer.BlockNorm)  # the constructor asks for a device
+    N.g_pre, N.g_post, N.d, N.res_scale, N.eps, N.flags = gain, gain if post else None, D, 1.0, 1e-6, 0
+    N.H_out, N.Xn = torch.zeros(28, D, dtype=BF16), torch.zeros(28, D, dtype=BF16)
+    N.Xq, N.amax, N.rstd = torch.zeros(28, D, dtype=I8), torch.zeros(28), torch.zeros(56)
+    N.dg_pre, N.dg_post = torch.zeros(D), torch.zeros(D) if post else None
+    N.ws_bytes, N.ws, N.T = 64, torch.zeros(64, dtype=torch.uint8), None
+    return N
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("Y", (2, 7, D)), ("Y", (28, D // 2)), ("Y", (7, 2 * D)), ("Y", (14 * D,)), ("Y", (1, 14, D)), ("Y", (29, D)),
+    ("H", (2, 7, D)), ("H", (28, D // 2)), ("H", (7, 2 * D)), ("H", (13, D)), ("gate", (2, 2 * D)),
+    ("gate", (4, D // 2)), ("gate", (1, 2, D)), ("gate", (1, D)),
+])
+def test_block_norm_forward_refuses_other_shapes(calls, name, bad):
+    N = _block_norm()
+    good = dict(Y=(14, D), H=(20, D), gate=(2, D))
+    types = dict(Y=torch.float32, H=BF16, gate=BF16)
+
+    def args(**over):
+        return {k: torch.zeros(*s, dtype=types[k]) for k, s in dict(good, **over).items()}
+
+    out = N.forward(**args(), gate_period=7, stream=0)
+    assert [tuple(x.shape) for x in out] == [(14, D)] * 3 + [(14,)] and len(calls) == 1
+    with pytest.raises(B.SblError):
+        N.forward(**args(**{name: bad}), gate_period=7, stream=0)
+    assert len(calls) == 1 and N.T == 14
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("dXn", (2, 7, D)), ("dXn", (13, D)), ("dXn", (7, 2 * D)), ("dH_out", (2, 7, D)), ("dH_out", (7, 2 * D)),
+    ("Y", (2, 7, D)), ("Y", (28, D // 2)), ("Y", (13, D)), ("dY", (14, 2 * D)), ("dY", (14, 1, D)), ("dH", (13, D)),
+    ("dH", (2, 7, D)), ("gate", (2, 2 * D)), ("dgate", (2, 2 * D)), ("dgate", (4, D // 2)),
+])
+def test_block_norm_backward_refuses_other_shapes(calls, name, bad):
+    N = _block_norm()
+    N.T = 14
+    good = dict(dXn=(14, D), dH_out=(14, D), Y=(14, D), dY=(14, D), dH=(14, D), gate=(2, D), dgate=(2, D))
+    f32 = ("dXn", "Y", "dgate")
+
+    def args(**over):
+        a = {k: torch.zeros(*s, dtype=torch.float32 if k in f32 else BF16) for k, s in dict(good, **over).items()}
+        return dict(a, dXn=[a["dXn"]])
+
+    N.backward(**args(), gate_period=7, stream=0)
+    N.backward(**dict(args(), dH_out=None, dH=None, gate=None, dgate=None), stream=0)
+    assert len(calls) == 2
+    with pytest.raises(B.SblError):
+        N.backward(**args(**{name: bad}), gate_period=7, stream=0)
+    assert len(calls) == 2
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("Xq", (2, 7, D)), ("Xq", (28, D // 2)), ("Xq", (7, 2 * D)), ("Xq", (14 * D,)), ("amax", (13,)),
+    ("Y", (2, 7, D_OUT)), ("Y", (13, D_OUT)), ("Y", (7, 2 * D_OUT)), ("dY", (2, 7, D_OUT)), ("dY", (7, 2 * D_OUT)),
+    ("X", (2, 7, D)), ("X", (13, D)), ("X", (7, 2 * D)), ("dX", (2, 7, D)), ("dX", (13, D)),
+    ("dW", (D, D_OUT)), ("dW", (2, D_OUT // 2, D)),
+])
+def test_int8_linear_refuses_other_shapes(calls, name, bad):
+    from semi_structured_sparsity_step_b200 import layer
+    L = object.__new__(layer.Int8Linear)
+    L.W, L.d_out, L.d_in = torch.zeros(D_OUT, D, dtype=BF16), D_OUT, D
+    L.Wq, L.wmax, L.one = torch.zeros(D_OUT, D, dtype=I8), torch.zeros(D_OUT), torch.ones(1)
+    fwd = dict(Xq=(14, D), amax=(14,), Y=(14, D_OUT))
+    bwd = dict(dY=(14, D_OUT), X=(14, D), dX=(14, D), dW=(D_OUT, D))
+    types = dict(Xq=I8, dY=BF16, X=BF16)
+
+    def args(good, **over):
+        return {k: torch.zeros(*s, dtype=types.get(k, torch.float32)) for k, s in dict(good, **over).items()}
+
+    L.forward(**args(fwd), stream=0)
+    L.backward(**args(bwd), stream=0)
+    L.backward(**dict(args(bwd), dX=None), stream=0)
+    L.backward(**dict(args(bwd), dW=None), stream=0)
+    L.backward(**args(bwd, dW=(D_OUT * D,)), stream=0)
+    L.forward(**args(fwd, amax=(20,), Y=(20, D_OUT)), stream=0)  # buffers for more tokens
+    assert len(calls) == 6
+    call, good = (L.forward, fwd) if name in fwd else (L.backward, bwd)
+    with pytest.raises(B.SblError):
+        call(**args(good, **{name: bad}), stream=0)
+    assert len(calls) == 6
