@@ -189,7 +189,9 @@ sbl_status sbl_grad_sqnorm(const float* dW, size_t n, double* sumsq, void* works
  * makes norm infinite and clip 0.
  * sbl_grad_norm_group writes S and norm; sbl_grad_clip_group writes S, norm,
  * clip and every out.  S is what sbl_adamw_step takes as grad_sqnorm, so
- * gradients that go to sbl_adamw_step alone need no clipped copy.
+ * gradients that go to sbl_adamw_step alone need no clipped copy.  It is the
+ * sum before the clip: gradients that were clipped go there with grad_sqnorm
+ * NULL, or they would be scaled twice.
  *   tensors    HOST array of `count` descriptors (read before the call
  *              returns; the pointers inside are device pointers, 16-byte
  *              aligned).  n >= 0 elements, any n; a tensor of n = 0 is

@@ -172,12 +172,18 @@ class Int8Linear:
 
 class GradClip:
     """The global norm of a step's gradients and the clip by it, over a fixed list of
-    tensors (fp32 or bf16), in place.  sumsq is what sbl_adamw_step takes as grad_sqnorm."""
+    tensors (fp32 or bf16), in place.
+
+    grad_sqnorm is what sbl_adamw_step takes under that name: after norm_only()
+    the sum of the squares, by which it clips itself; after clip(), whose
+    gradients are scaled already, None (sumsq is still the sum before the
+    clip, and would scale them a second time)."""
 
     def __init__(self, grads):
         self.tensors = [(g, g, g.numel(), g.dtype == torch.bfloat16) for g in grads]
         dev = grads[0].device
         self.sumsq = torch.zeros(1, dtype=torch.float64, device=dev)
+        self.grad_sqnorm = None
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.factor = torch.zeros(1, dtype=torch.float32, device=dev)
         self.ws_bytes = B.sbl_grad_group_workspace_bytes(len(grads))
@@ -185,7 +191,9 @@ class GradClip:
 
     def norm_only(self, stream=None):
         B.sbl_grad_norm_group(self.tensors, self.sumsq, self.norm, self.ws, self.ws_bytes, stream)
+        self.grad_sqnorm = self.sumsq
 
     def clip(self, max_norm: float, stream=None):
         B.sbl_grad_clip_group(self.tensors, max_norm, self.sumsq, self.norm, self.factor, self.ws, self.ws_bytes,
                               stream)
+        self.grad_sqnorm = None

@@ -189,3 +189,18 @@ def test_int8_linear_refuses_other_shapes(calls, name, bad):
     with pytest.raises(B.SblError):
         call(**args(good, **{name: bad}), stream=0)
     assert len(calls) == 6
+
+
+def test_clipped_gradients_are_not_clipped_again_by_the_optimizer(calls):
+    """sumsq stays the sum of the gradients as they came, so after a clip in place the optimizer gets none."""
+    from semi_structured_sparsity_step_b200 import layer
+    C = object.__new__(layer.GradClip)  # the constructor's tensors are on a device
+    g = torch.zeros(64)
+    C.tensors, C.ws, C.ws_bytes = [(g, g, 64, False)], torch.zeros(64, dtype=torch.uint8), 64
+    C.sumsq, C.norm, C.factor, C.grad_sqnorm = torch.zeros(1, dtype=torch.float64), torch.zeros(1), torch.zeros(1), None
+    for _ in range(2):
+        C.norm_only(stream=0)
+        assert C.grad_sqnorm is C.sumsq
+        C.clip(1.0, stream=0)
+        assert C.grad_sqnorm is None
+    assert [c[0] for c in calls] == ["sbl_grad_norm_group", "sbl_grad_clip_group"] * 2
