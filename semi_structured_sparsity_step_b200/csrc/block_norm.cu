@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(bn_threads(TPR), bn_blocks(TPR, VPT)) block_no
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int i = tr + k * TPR;
-        to[k] = i < a.nv ? __ldg(p + i) : make_uint2(0u, 0u);
+        to[k] = i < a.nv ? pdl::load(p + i) : make_uint2(0u, 0u);
       }
     };
     if (a.gate != nullptr) fetch(a.gate + static_cast<long long>(rc / a.period) * a.nv, gate);

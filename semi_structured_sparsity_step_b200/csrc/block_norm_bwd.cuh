@@ -175,8 +175,8 @@ __global__ void __launch_bounds__(bb_threads(TPR), bb_blocks_per_sm(TPR)) block_
     const int i = tr + k * TPR;
     gpre[k] = gpost[k] = make_uint2(0x3F803F80u, 0x3F803F80u);  // 1.0
     if (i < my_vecs) {
-      gpre[k] = __ldg(a.g_pre + first_vec + i);
-      if constexpr (POST) gpost[k] = __ldg(a.g_post + first_vec + i);
+      gpre[k] = a.g_pre[first_vec + i];
+      if constexpr (POST) gpost[k] = a.g_post[first_vec + i];
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -193,8 +193,8 @@ __global__ void __launch_bounds__(bb_threads(TPR), bb_blocks_per_sm(TPR)) block_
       const int row = w.row + step;
       float r1 = 1.0f, r2 = 0.0f;
       if (active) {
-        if constexpr (POST) r1 = __ldg(a.rstd + row);
-        r2 = __ldg(a.rstd + a.T + row);
+        if constexpr (POST) r1 = a.rstd[row];
+        r2 = a.rstd[static_cast<long long>(a.T) + row];
       }
       const uint8_t* staged = slots + static_cast<size_t>(pos.slot) * a.slot_bytes;
       const uint8_t* s_dh = a.dH_in != nullptr ? staged + off_dh : reinterpret_cast<const uint8_t*>(&s_zero);

@@ -794,7 +794,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<kI8, kAMN, kBMN
       int pi, mb, nb, sp;
       grp.locate(w, pi, mb, nb, sp);
       const int c = nb * C::BN + et;
-      wmax_next = c < grp.args[pi].N ? __ldg(grp.args[pi].wmax + c) : 0.0f;
+      wmax_next = c < grp.args[pi].N ? grp.args[pi].wmax[c] : 0.0f;
     };
     if constexpr (epi_w8(EPI)) fetch_wmax(pair_id);
     int t = 0;

@@ -136,7 +136,7 @@ __device__ __forceinline__ double tile_sumsq(const void* g, unsigned long long n
 
 // keep: tiles at the end of the table that L2 should hold until the scaling pass.
 __global__ void __launch_bounds__(kGgThreads) grad_sumsq_kernel(const __grid_constant__ GradTable tab,
-                                                                double* __restrict__ partial, unsigned keep) {
+                                                                double* partial, unsigned keep) {
   __shared__ double scratch[kGgThreads / 32];
   pdl::wait();
   pdl::release();
@@ -175,7 +175,7 @@ __device__ __forceinline__ void store_norm(double S, float c, double* sumsq, flo
   }
 }
 
-__global__ void __launch_bounds__(kGgThreads) grad_norm_finish_kernel(const double* __restrict__ partial, int count,
+__global__ void __launch_bounds__(kGgThreads) grad_norm_finish_kernel(const double* partial, int count,
                                                                       double* sumsq, float* norm) {
   __shared__ double scratch[kGgThreads / 32];
   pdl::wait();
@@ -227,7 +227,7 @@ __device__ __forceinline__ void tile_scale(const void* g, void* out, unsigned lo
 }
 
 __global__ void __launch_bounds__(kGgThreads)
-    grad_scale_kernel(const __grid_constant__ GradTable tab, const double* __restrict__ partial, int partials,
+    grad_scale_kernel(const __grid_constant__ GradTable tab, const double* partial, int partials,
                       double max_norm, double* sumsq, float* norm, float* clip) {
   __shared__ double scratch[kGgThreads / 32];
   pdl::wait();

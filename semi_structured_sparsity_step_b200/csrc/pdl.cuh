@@ -3,14 +3,25 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <cstdint>
 
 namespace sbl {
 
 // Programmatic dependent launch: a kernel may be set up while the previous one of its stream
-// finishes, and touches global memory only after wait().
+// finishes, and touches global memory only after wait().  Loads behind it are ordinary ones: memory that the
+// previous kernel writes is not constant for this kernel's life, as a read-only load (__ldg) asks for
+// and a __restrict__ pointer lets the compiler assume, which could then move it ahead of wait().
 namespace pdl {
 
 __device__ __forceinline__ void wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Load that stays behind wait(), by its place among volatile statements, and that the compiler may still take
+// ahead of the kernel's own stores: a plain one could alias them.
+__device__ __forceinline__ uint2 load(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
 
 // The next kernel may be set up once every block has called this or ended.  Called behind wait(), so that
 // a kernel that reads ahead of its own wait (the decode GEMVs read packed weights) finds whole what
