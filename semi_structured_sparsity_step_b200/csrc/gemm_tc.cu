@@ -583,7 +583,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<kI8, kAMN, kBMN
   const int n_pairs = gridDim.x >> 1;
   const uint32_t peer_abort = pair::map_to(smem_u32(const_cast<int*>(abort_flag)), rank ^ 1u);
 
-  if (threadIdx.x == 0) pdl_launch_dependents();
+  if constexpr (!epi_w8(EPI)) {
+    if (threadIdx.x == 0) pdl_launch_dependents();
+  }
   if constexpr (KP > 0) {
     for (int i = threadIdx.x; i < 256; i += blockDim.x) {
       uint32_t s0, s1;
@@ -620,6 +622,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg2<kI8, kAMN, kBMN
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();
+  if constexpr (epi_w8(EPI)) {  // as the short-batch form does (pdl.cuh has the reason)
+    if (threadIdx.x == 0) pdl_launch_dependents();
+  }
 
   auto give_up = [&]() {
     *abort_flag = 1;

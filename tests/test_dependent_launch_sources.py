@@ -25,3 +25,16 @@ def test_nothing_is_read_as_constant_for_the_kernel_s_life(name):
 
 def test_scales_of_the_tensor_core_products_are_no_read_only_loads():
     assert re.findall(r"__ldg\s*\([^;]*\b(?:amax|wmax|gamma)\b", _code("gemm_tc.cu")) == []
+
+
+def test_the_8_bit_product_releases_its_successor_behind_its_own_wait():
+    """The decode products read packed weights ahead of their wait, which holds only where every kernel before
+    them had waited when it released them: the full-batch form of the 8-bit product too."""
+    code = _code("gemm_tc.cu")
+    body = code[code.index("tc_gemm_pair_kernel("):]
+    wait = body.index("pdl_wait();")
+    before, after = body[:wait], body[wait:]
+    assert before.count("pdl_launch_dependents()") == \
+        len(re.findall(r"if constexpr \(!epi_w8\(EPI\)\) \{\s*if \([^;{}]*\) pdl_launch_dependents\(\);\s*\}", before))
+    assert re.match(r"pdl_wait\(\);\s*if constexpr \(epi_w8\(EPI\)\) \{\s*if \([^;{}]*\) pdl_launch_dependents\(\);\s*\}",
+                    after)
