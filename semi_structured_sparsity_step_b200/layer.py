@@ -123,7 +123,10 @@ class BlockNorm:
         assert dY.shape[0] == self.T  # the factors lie as that many tokens left them
         _rows_of("sbl_block_norm_backward", self.d, *dXn, dH_out, Y, dY, dH, gate, dgate)
         if self.ws is None:
-            self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
+            # of the stream that writes it: memory freed on the current one may still be read there
+            s = torch.cuda.ExternalStream(stream, device=self.g_pre.device) if isinstance(stream, int) else stream
+            with torch.cuda.stream(s):
+                self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.g_pre.device)
         B.sbl_block_norm_backward(dXn, dH_out, Y, self.H_out, self.g_post, gate, gate_period, self.res_scale,
                                   self.g_pre, self.rstd, dY.shape[0], self.d, self.flags, dY, dH, self.dg_post,
                                   self.dg_pre, dgate, int(accumulate), self.ws, self.ws_bytes, stream)

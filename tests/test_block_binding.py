@@ -204,3 +204,35 @@ def test_clipped_gradients_are_not_clipped_again_by_the_optimizer(calls):
         C.clip(1.0, stream=0)
         assert C.grad_sqnorm is None
     assert [c[0] for c in calls] == ["sbl_grad_norm_group", "sbl_grad_clip_group"] * 2
+
+
+@pytest.mark.parametrize("stream", ["none", "object", "handle"])
+def test_workspace_of_the_first_backward_belongs_to_its_stream(calls, monkeypatch, stream):
+    """Allocated under another stream, it could be memory whose last reader there still runs."""
+    from contextlib import contextmanager
+    from types import SimpleNamespace
+    from semi_structured_sparsity_step_b200 import layer
+    current, allocated = ["the caller's"], []
+
+    @contextmanager
+    def use(s):
+        current.append(current[-1] if s is None else s)
+        yield
+        current.pop()
+
+    def empty(*size, **kw):
+        allocated.append(current[-1])
+        return torch.empty(*size, dtype=kw["dtype"])
+
+    monkeypatch.setattr(layer, "torch", SimpleNamespace(
+        empty=empty, uint8=torch.uint8, cuda=SimpleNamespace(
+            stream=use, ExternalStream=lambda handle, device=None: ("external", handle))))
+    side = SimpleNamespace(cuda_stream=1234)
+    arg, owner = {"none": (None, "the caller's"), "object": (side, side), "handle": (1234, ("external", 1234))}[stream]
+    monkeypatch.setattr(B, "_stream", lambda s: 0)
+    N = _block_norm()
+    N.T, N.ws = 14, None
+    x, h = torch.zeros(14, D), torch.zeros(14, D, dtype=BF16)
+    for _ in range(2):
+        N.backward([x], None, x, h, None, stream=arg)
+    assert allocated == [owner] and len(calls) == 2
