@@ -188,7 +188,7 @@ __device__ __forceinline__ bool bar_any(bool x) {
   return any != 0u;
 }
 
-// The same for the 8-bit product: scale (the token's) and sw (the columns', in shared memory) both in
+// epilogue_chunk for the 8-bit product: scale (the token's) and sw (the columns', in shared memory) both in
 // the row layout.  A bf16 chunk is packed before it is turned around, and two of them are, so that a row's
 // segment is 128 bytes in either type.
 __device__ __forceinline__ void scaled_w8_bf16(uint32_t* t, const uint32_t (&r)[32], float scale, const float* sw) {

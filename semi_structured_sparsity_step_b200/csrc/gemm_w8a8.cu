@@ -280,7 +280,9 @@ struct W8Plan {
 
 // The fastest by a model of the time in ns, fitted to 458 cases (T 1 .. 8192, d_in 128 .. 11008, d_out
 // 128 .. 32768, both types), on which the plan it picks is 1.1% above the fastest of all token tiles and
-// splits on average, and more than 10% above it in 14 cases (the worst 19%):
+// splits on average, and more than 10% above it in 14 cases (the worst 19%).  It is fitted to order the plans; a
+// time that it gives can be further off (422 x 3536 -> 10328, 82 tiles of 256 x 256 on 74 pairs: 19 us given,
+// 30 to 33 measured):
 //   streaming kernel: 4000 for the launch, plus the longest of
 //     what an SM copies from L2 (its blocks x their K blocks x 16 KB + 128 BN) at 186 bytes/ns, 89 with
 //     more than one block on it, 168 at BN 256,

@@ -12,8 +12,13 @@
 // same order, so no block waits for another) and scales.  The scaling pass walks the tiles
 // backwards, so it starts with what the norm pass read last and left in L2; gradients that fit
 // there are read from HBM once.  No atomics: S is the same bits for the same tensors on every run on
-// one device.  Measured: norm pass alone 173 us for 1233 MB (7.1 TB/s), with clipping 550 us, where
-// reading all but 64 MB twice and writing once takes 555 us at the measured copy rate.
+// one device.  More than 128 tensors take several tables, a launch each: both passes go through the tables
+// forwards, and backwards only within one, so there the scaling pass starts with the table that was
+// read first and finds little of it in L2.
+// Measured: norm pass alone 173 us for 1233 MB (7.1 TB/s), with clipping 550 us, where
+// reading all but 64 MB twice and writing once takes 555 us at the measured copy rate.  Whole models, bf16, out of
+// place: 716 MB in 216 tensors 339 us (two reads and a write at the copy rate 328), 5549 MB in 324 tensors
+// 2518 us (2542); 418 MB in 126 tensors, one table, 190 us (191).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstdint>
@@ -27,8 +32,8 @@ namespace {
 constexpr int kGgThreads = 256;
 constexpr int kGgVecs = 4;                            // 16-byte vectors per thread and tile
 constexpr int kGgTileVecs = kGgThreads * kGgVecs;     // 16 KB per tile
-// The scaling pass is to find this much of the norm pass's last reads in L2; what is read before goes
-// first.  Measured on gradients of 308 MB: 144.5 us, with 32 or 128 MB 147.6, with plain loads 152.5
+// The scaling pass is to find this much of the norm pass's last reads in L2 (of each table's, where there are
+// several); what is read before goes first.  Measured on gradients of 308 MB: 144.5 us, with 32 or 128 MB 147.6, with plain loads 152.5
 // (136.8 with the scaling pass as it is now).
 constexpr unsigned kGgKeepTiles = (64u << 20) / (kGgTileVecs * 16);
 constexpr int kGgTensors = 128;                       // tensors per launch (the table is a kernel parameter)
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kGgThreads)
 constexpr int kGgBlocksPerSm = 4;
 // Tiles per block of the scaling pass.  Blocks that come one after the other walk the memory more evenly
 // than four per SM that stay: 1233 MB 550 us against 593 (6.4 against 5.7 TB/s of that pass); a block
-// reads the partial sums (5 KB, in L2) for two tiles.  In place the blocks stay: below the limit there
+// reads the partial sums (in L2, 5 KB for each table of up to 128 tensors) for two tiles.  In place the blocks stay: below the limit there
 // is nothing to scale, and 38000 blocks that find that out take 50 us, 592 take 3.
 constexpr unsigned kGgScaleTiles = 2;
 constexpr int kGgMaxBlocks = 1024;  // of one launch: sizes the workspace
