@@ -348,7 +348,10 @@ sbl_status sbl_rmsnorm_act_quant(const void* X, const void* g, float eps, int T,
  *   dY = r1 * (du * g_post - yh * mean(du * g_post * yh))    (du without g_post),
  *   dg_pre = sum_t dxn * xh,  dg_post = sum_t du * yh.
  * fp32 arithmetic, fixed summation order (the same bits on every run), one
- * rounding where an output is bf16.
+ * rounding where an output is bf16.  The sums over tokens (dg_pre, dg_post,
+ * dgate) add at most T / L rows in sequence, then partial rows, with L = 1 (wide
+ * rows) to 16 (narrow ones) row lanes per SM: their error is at most about
+ * (T / L + L / 4 + 80) 2^-24 of the sum of the absolute terms, and grows with T.
  *   dXn        HOST array of `readers` (1..3) device pointers, [T, d] float
  *              each: the dX of the products that read xn (sbl_backward).
  *   dH_out     optional (NULL: zero): [T, d], type of H: the gradient of h'

@@ -16,7 +16,7 @@
 // y^2, sum of h'^2, max |xn|); gains and gate rows come from L1/L2.  The reductions are a chain of
 // barriers, so the rows to come are kept on their way: each group of TPR threads has a ring of
 // staged rows in shared memory, filled by bulk copies, and refills a slot once its row is in
-// registers.  Measured: 32768 x 2048 (y fp32, h bf16, a gate per sequence) 123 us, 0.91 of the measured
+// registers.  Measured: 32768 x 2048 (y fp32, h bf16, a gate per sequence) 124 us, 0.91 of the measured
 // copy rate; one row of 2048 2.4 us, a launch and the chain of three sums.  With 8 columns per thread
 // instead of 32 the large case took 185 us: it is the instructions that every thread spends once per
 // row that have to be few.

@@ -20,7 +20,7 @@
 // Every mbarrier wait is bounded (sbl_device.cuh).
 //
 // Measured: 1 x 11008 x 32768 (361 MB of weights) 55.6 us, the measured copy rate; 1 x 2048 x 11008
-// 6.3 us and 509 x 2048 x 2048 7.6 us with the operands in L2, of which about 3 us are the launch and
+// 6.4 us and 509 x 2048 x 2048 7.4 us with the operands in L2, of which about 3 us are the launch and
 // the first copy's latency.
 #include <cuda.h>
 #include <cuda_bf16.h>
