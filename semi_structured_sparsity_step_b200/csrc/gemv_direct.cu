@@ -40,6 +40,7 @@
 #include <cstdint>
 
 #include "packed_decode.cuh"
+#include "pdl.cuh"
 #include "sbl_device.cuh"
 #include "sbl_internal.h"
 
@@ -142,7 +143,7 @@ __device__ __forceinline__ void load_x(uint4 (&xv)[NT][4], const int8_t* const (
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      xv[n][q] = (tv[n] && c + 2 * q < nchunks) ? __ldg(reinterpret_cast<const uint4*>(xr[n] + 8 * (c + 2 * q)))
+      xv[n][q] = (tv[n] && c + 2 * q < nchunks) ? pdl::load(reinterpret_cast<const uint4*>(xr[n] + 8 * (c + 2 * q)))
                                                 : make_uint4(0u, 0u, 0u, 0u);
 }
 

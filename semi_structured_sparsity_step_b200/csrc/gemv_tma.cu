@@ -53,6 +53,7 @@
 #include <cstdint>
 
 #include "packed_decode.cuh"
+#include "pdl.cuh"
 #include "sbl_device.cuh"
 #include "sbl_internal.h"
 
@@ -178,11 +179,11 @@ __device__ __forceinline__ void x_fetch(uint4 (&xv)[NT][4], const Walk<NT>& w, i
     const uint4* p = reinterpret_cast<const uint4*>(w.xr[m] + 8 * c);
     if (tv[m] && c + 8 <= w.nchunks) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) xv[m][q] = SH ? p[q] : __ldg(p + q);
+      for (int q = 0; q < 4; ++q) xv[m][q] = SH ? p[q] : pdl::load(p + q);
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        xv[m][q] = (tv[m] && c + 2 * q < w.nchunks) ? (SH ? p[q] : __ldg(p + q)) : make_uint4(0u, 0u, 0u, 0u);
+        xv[m][q] = (tv[m] && c + 2 * q < w.nchunks) ? (SH ? p[q] : pdl::load(p + q)) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }

@@ -28,6 +28,7 @@
 #include <cstdint>
 
 #include "packed_decode.cuh"
+#include "pdl.cuh"
 #include "sbl_device.cuh"
 #include "sbl_internal.h"
 
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(kGemvThreads, 2)
         for (int q = 0; q < 4; ++q) {
           xv[n][q] = make_uint4(0u, 0u, 0u, 0u);
           if (tv[n] && chl + 2 * q < nchunks)
-            xv[n][q] = __ldg(reinterpret_cast<const uint4*>(xr[n] + static_cast<size_t>(chl + 2 * q) * 8));
+            xv[n][q] = pdl::load(reinterpret_cast<const uint4*>(xr[n] + static_cast<size_t>(chl + 2 * q) * 8));
         }
       if (!mbar_wait_sleep(&s_full[s], static_cast<uint32_t>(it / Tl::STAGES) & 1u, &s_abort, err)) {
         ok = false;

@@ -22,6 +22,11 @@ __device__ __forceinline__ uint2 load(const uint2* p) {
   asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
+__device__ __forceinline__ uint4 load(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 
 // The next kernel may be set up once every block has called this or ended.  Called behind wait(), so that
 // a kernel that reads ahead of its own wait (the decode GEMVs read packed weights) finds whole what

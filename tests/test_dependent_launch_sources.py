@@ -38,3 +38,10 @@ def test_the_8_bit_product_releases_its_successor_behind_its_own_wait():
         len(re.findall(r"if constexpr \(!epi_w8\(EPI\)\) \{\s*if \([^;{}]*\) pdl_launch_dependents\(\);\s*\}", before))
     assert re.match(r"pdl_wait\(\);\s*if constexpr \(epi_w8\(EPI\)\) \{\s*if \([^;{}]*\) pdl_launch_dependents\(\);\s*\}",
                     after)
+
+
+@pytest.mark.parametrize("name", ["gemv_direct.cu", "gemv_tma.cu", "pack_gemv.cu"])
+def test_activations_of_the_decode_products_are_no_read_only_loads(name):
+    """Codes that the block norm writes while the product behind it is already there."""
+    loads = re.findall(r"__ldg\s*\([^;]*", _code(name))
+    assert [x for x in loads if re.search(r"\bxr\b|\bp \+ q\b", x)] == []
