@@ -67,11 +67,11 @@ def act_quant(X: torch.Tensor, Xq: torch.Tensor, amax: torch.Tensor, stream=None
 
 
 def _rows_of(fn, width, *tensors):
-    """Refuses tensors that are not [rows, width].  A call takes a contiguous buffer of at least as many
+    """Refuses tensors that are not [rows, width], or [width] for one row.  A call takes a contiguous buffer of at least as many
     elements as it has tokens: it would read [batch, sequence, width] as its first rows, and halves of
     wider rows as rows.  A buffer may hold more rows than the call has tokens; they stay as they are."""
     for x in tensors:
-        if x is not None and x.__class__ is not int and (x.dim() != 2 or x.shape[1] != width):
+        if x is not None and x.__class__ is not int and (x.dim() not in (1, 2) or x.shape[-1] != width):
             raise B.SblError(fn, 2)
 
 
@@ -83,9 +83,9 @@ class BlockNorm:
     None: the branch is not normalised).  The outputs and the factors that the
     backward needs live here and are overwritten by the next call.
 
-    Activations and their gradients are [tokens, d], gates [rows, d], with as
-    many tokens as Y has (a [batch, sequence, d] is flattened by the caller);
-    tensors of other dimensions or widths raise SblError."""
+    Activations and their gradients are [tokens, d], with as many tokens as Y
+    has (a [batch, sequence, d] is flattened by the caller), gates [rows, d] or
+    [d] for one row; tensors of other dimensions or widths raise SblError."""
 
     def __init__(self, g_pre: torch.Tensor, g_post: torch.Tensor | None = None, max_tokens: int = 1,
                  res_scale: float = 1.0, eps: float = 1e-6, y_dtype=torch.float32, h_dtype=torch.bfloat16):

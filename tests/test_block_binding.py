@@ -120,7 +120,8 @@ def _block_norm(post=True):
 @pytest.mark.parametrize("name,bad", [
     ("Y", (2, 7, D)), ("Y", (28, D // 2)), ("Y", (7, 2 * D)), ("Y", (14 * D,)), ("Y", (1, 14, D)), ("Y", (29, D)),
     ("H", (2, 7, D)), ("H", (28, D // 2)), ("H", (7, 2 * D)), ("H", (13, D)), ("gate", (2, 2 * D)),
-    ("gate", (4, D // 2)), ("gate", (1, 2, D)), ("gate", (1, D)),
+    ("gate", (4, D // 2)), ("gate", (1, 2, D)), ("gate", (1, D)), ("gate", (D,)), ("gate", (2 * D,)), ("Y", (D,)),
+    ("H", (D,)),
 ])
 def test_block_norm_forward_refuses_other_shapes(calls, name, bad):
     N = _block_norm()
@@ -131,10 +132,12 @@ def test_block_norm_forward_refuses_other_shapes(calls, name, bad):
         return {k: torch.zeros(*s, dtype=types[k]) for k, s in dict(good, **over).items()}
 
     out = N.forward(**args(), gate_period=7, stream=0)
-    assert [tuple(x.shape) for x in out] == [(14, D)] * 3 + [(14,)] and len(calls) == 1
+    assert [tuple(x.shape) for x in out] == [(14, D)] * 3 + [(14,)]
+    N.forward(**args(gate=(D,)), gate_period=14, stream=0)  # a gate for each channel
+    assert len(calls) == 2
     with pytest.raises(B.SblError):
         N.forward(**args(**{name: bad}), gate_period=7, stream=0)
-    assert len(calls) == 1 and N.T == 14
+    assert len(calls) == 2 and N.T == 14
 
 
 @pytest.mark.parametrize("name,bad", [
