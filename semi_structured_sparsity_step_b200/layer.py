@@ -167,7 +167,8 @@ class Int8Linear:
         f32, bf16 = torch.float32, torch.bfloat16
         n = self.d_out * self.d_in
         _rows_of("sbl_backward", self.d_out, dY)
-        _rows_of("sbl_backward", self.d_in, X, dX, dW if dW is None or dW.dim() != 1 else None)
+        flat = isinstance(dW, torch.Tensor) and dW.dim() == 1
+        _rows_of("sbl_backward", self.d_in, X, dX, None if flat else dW)
         B.sbl_backward(a(dY, bf16, T * self.d_out), a(X, bf16, T * self.d_in), a(self.W, bf16, n), self.one, T,
                        self.d_in, self.d_out, a(dX, f32, T * self.d_in), a(dW, f32, n), int(accumulate_dW), None, 0,
                        stream)

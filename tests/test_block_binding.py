@@ -186,12 +186,13 @@ def test_int8_linear_refuses_other_shapes(calls, name, bad):
     L.backward(**dict(args(bwd), dX=None), stream=0)
     L.backward(**dict(args(bwd), dW=None), stream=0)
     L.backward(**args(bwd, dW=(D_OUT * D,)), stream=0)
+    L.backward(**dict(args(bwd), dW=1 << 12), stream=0)  # a raw pointer
     L.forward(**args(fwd, amax=(20,), Y=(20, D_OUT)), stream=0)  # buffers for more tokens
-    assert len(calls) == 6
+    assert len(calls) == 7
     call, good = (L.forward, fwd) if name in fwd else (L.backward, bwd)
     with pytest.raises(B.SblError):
         call(**args(good, **{name: bad}), stream=0)
-    assert len(calls) == 6
+    assert len(calls) == 7
 
 
 def test_clipped_gradients_are_not_clipped_again_by_the_optimizer(calls):
